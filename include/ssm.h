@@ -412,6 +412,164 @@ ssm_status ssm_ssd_chunk_scan(const ssm_ssd_dims *dims, const void *cb, const vo
                               void *out, void *stream);
 
 /*
+ * Gated delta rule -- a matrix-state recurrence of the same family as the
+ * scans above, with an erase term: per sequence and head, with state S in
+ * R^{dv x dk}, a_t = exp(g_t) and u_t in R^dv,
+ *
+ *   u_t = beta_t (v_t - a_t S_{t-1} k_t)
+ *   S_t = a_t S_{t-1} + u_t k_t^T
+ *   o_t = scale S_t q_t
+ *
+ * Head h reads key group h / (nheads / ngroups), as in ssm_ssd_chunk_scan.
+ * With qk_l2norm, q_t and k_t are first divided by sqrt(sum of squares + 1e-6).
+ *
+ * Types. q, k, v, out: bf16; g, beta, states and all sums: fp32. g is a log
+ * decay and is meant to be <= 0 (a g below -177 resets the state: its decay is
+ * 0 in fp32); a positive g is computed by the same formula as long as the
+ * decays within 64 tokens stay in fp32 range.
+ *
+ * Shapes. d_key a multiple of 8 in [8, 128], d_value a multiple of 8 in
+ * [8, 4096] (SSM_ERR_UNSUPPORTED otherwise); nheads a multiple of ngroups.
+ * Pointers of q, k, v, out and the states are 16-byte aligned, g, beta,
+ * cu_seqlens and state_index 4-byte aligned. Strides are in elements, 0 = the
+ * dense default; those of q, k, v and out are multiples of 8 and the last two
+ * dimensions (head, channel) are dense:
+ *   q, k   element (s, t, g, i) at s*seq_stride + t*tok_stride + g*d_key + i
+ *   v, out element (s, t, h, i) at s*seq_stride + t*tok_stride + h*d_value + i
+ *   g, beta        (s, t, h)    at s*gb_seq_stride + t*gb_tok_stride + h
+ */
+typedef struct {
+  int64_t batch;   /* sequences (> 0) */
+  int64_t seqlen;  /* tokens per sequence (>= 0); with cu_seqlens: tokens of the packed buffer; decode ignores it */
+  int64_t nheads, ngroups, d_key, d_value;
+  float scale;       /* 0 = 1 / sqrt(d_key) */
+  int32_t qk_l2norm; /* 0 or 1 */
+  int64_t q_tok_stride, q_seq_stride;
+  int64_t k_tok_stride, k_seq_stride;
+  int64_t v_tok_stride, v_seq_stride;
+  int64_t out_tok_stride, out_seq_stride;
+  int64_t gb_tok_stride, gb_seq_stride;
+} ssm_delta_dims;
+
+/*
+ * ssm_delta_prefill -- the rule over whole sequences.
+ *   q, k        [b, L, ngroups, d_key] bf16; v [b, L, nheads, d_value] bf16
+ *   g, beta     [b, L, nheads] fp32
+ *   cu_seqlens  NULL, or [batch + 1] int32 on the device, non-decreasing from 0:
+ *               sequence s is rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 of
+ *               packed [T, ...] buffers (T = seqlen; the sequence strides are
+ *               not used). A sequence may be empty. Entries are clamped to
+ *               [0, T]; rows of no sequence are neither read for a result nor
+ *               written.
+ *   state_in    [b, nheads, d_value, d_key] fp32, dense, or NULL = zeros
+ *   out         [b, L, nheads, d_value] bf16; must not overlap the inputs
+ *   state_out   [b, nheads, d_value, d_key] fp32, dense: the state after the
+ *               last token; may be state_in
+ *   workspace   ssm_delta_prefill_workspace_bytes(dims) bytes of device
+ *               scratch, 256-byte aligned, or NULL when that is 0. Calls that
+ *               overlap on the GPU need separate workspaces.
+ * A long sequence may be processed in pieces: feeding one call's state_out to
+ * the next gives the result of one call up to fp32 rounding.
+ */
+size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims *dims);
+ssm_status ssm_delta_prefill(const ssm_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
+                             const float *beta, const int32_t *cu_seqlens, const float *state_in, void *out,
+                             float *state_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * ssm_delta_decode_step -- the rule over one token per sequence.
+ *   q, k [b, ngroups, d_key] bf16, v [b, nheads, d_value] bf16, g, beta
+ *   [b, nheads] fp32, out [b, nheads, d_value] bf16: row s at its seq stride
+ *   (the token strides are not used; dense defaults without L).
+ *   state_index NULL (row s uses state s), or [b] int32 on the device: row s
+ *               uses state state_index[s] of a pool of num_states. A row whose
+ *               index is negative or >= num_states is padding: neither its
+ *               output nor any state is touched. Two rows of one call must not
+ *               name the same state (which of them it then keeps is not
+ *               specified).
+ *   state_in    [num_states, nheads, d_value, d_key] fp32, dense
+ *   state_out   the same shape; state_in itself for an update in place, or
+ *               another pool (states of rows not named are left as they are).
+ * num_states >= batch when state_index is NULL.
+ */
+ssm_status ssm_delta_decode_step(const ssm_delta_dims *dims, const void *q, const void *k, const void *v,
+                                 const float *g, const float *beta, const int32_t *state_index, int64_t num_states,
+                                 const float *state_in, void *out, float *state_out, void *stream);
+
+/*
+ * ssm_gated_norm -- the norm between a scan and out_proj, fused with its gate.
+ * Per row and group of `group` consecutive channels, rms(x)^2 = mean(x^2) + eps:
+ *   gate_first = 0:  y = x / rms(x) * w * SiLU(z)
+ *   gate_first = 1:  t = x * SiLU(z),  y = t / rms(t) * w
+ * x, z, y [b, L, dim] io_dtype, element (s, t, e) at s*seq_stride +
+ * t*tok_stride + e (strides 0 = dense, any value >= 0; token strides >= dim);
+ * z may be NULL (no gate). w fp32: [dim], or [group] for every group alike
+ * with shared_weight. y may be x or z (same strides). dim a multiple of group,
+ * group <= 32768 (SSM_ERR_UNSUPPORTED above). fp32 sums; y rounded once.
+ * Pointers need only their element's alignment; 16-byte aligned pointers with
+ * strides and group multiples of 8 take vector loads.
+ */
+typedef struct {
+  int64_t batch, seqlen, dim, group;
+  float eps;
+  int32_t io_dtype; /* ssm_dtype of x, z, y */
+  int32_t gate_first, shared_weight;
+  int64_t x_tok_stride, x_seq_stride;
+  int64_t z_tok_stride, z_seq_stride;
+  int64_t y_tok_stride, y_seq_stride;
+} ssm_gated_norm_dims;
+
+ssm_status ssm_gated_norm(const ssm_gated_norm_dims *dims, const void *x, const void *z, const float *w, void *y,
+                          void *stream);
+
+/*
+ * ssm_residual_norm -- the step between two blocks: the norm behind one block
+ * (optional), its residual scale and addition, and the norm before the next,
+ * in one pass. Per row of `dim` channels:
+ *   t  = x,  or  x / rms(x) * post_w  where post_w is given
+ *   r' = residual_in + residual_scale * t     (residual_in NULL = 0)
+ *   y  = r' / rms(r') * w
+ * x, y [rows, dim] io_dtype; residual_in, residual_out [rows, dim]
+ * residual_dtype; row strides in elements (0 = dim); w, post_w [dim] fp32.
+ * y is the norm of r' before its rounding to residual_dtype. residual_out may
+ * be residual_in (same stride) and may be NULL (not written); y may be x.
+ * dim <= 32768 (SSM_ERR_UNSUPPORTED above). Alignment as for ssm_gated_norm.
+ */
+typedef struct {
+  int64_t rows, dim;
+  float eps, residual_scale;
+  int32_t io_dtype, residual_dtype; /* ssm_dtype */
+  int64_t x_stride, residual_in_stride, y_stride, residual_out_stride;
+} ssm_residual_norm_dims;
+
+ssm_status ssm_residual_norm(const ssm_residual_norm_dims *dims, const void *x, const void *residual_in,
+                             const float *w, const float *post_w, void *y, void *residual_out, void *stream);
+
+/*
+ * ssm_residual_block_forward -- one pre-norm residual layer around the block:
+ *   (hidden, residual_out) = ssm_residual_norm(x, residual_in)
+ *   out                    = ssm_block_forward(hidden)
+ * x is the previous block's output (or the embedding, with residual_in NULL):
+ * the next layer takes out as its x and residual_out as its residual_in.
+ *   x, out        [b, L, D] bf16, dense;  norm->w, norm->post_w (or NULL) [D] fp32
+ *   residual_in (or NULL), residual_out  [b, L, D] norm->residual_dtype, dense
+ *   workspace     ssm_residual_block_workspace_bytes(dims) bytes, 256-byte aligned
+ * The other arguments are those of ssm_block_forward. out may be x.
+ */
+typedef struct {
+  const float *w, *post_w;
+  float eps, residual_scale;
+  int32_t residual_dtype;
+} ssm_block_norm;
+
+size_t ssm_residual_block_workspace_bytes(const ssm_block_dims *dims);
+ssm_status ssm_residual_block_forward(const ssm_block_dims *dims, const ssm_weights *w, const ssm_block_weights *proj,
+                                      const ssm_block_norm *norm, const void *x, const void *residual_in,
+                                      const void *conv_cache_in, const float *ssm_state_in, void *residual_out,
+                                      void *out, void *conv_cache_out, float *ssm_state_out, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
  * Sequence-parallel prefill -- one sequence split into segments that are
  * computed at the same time (one per GPU, or pieces of one long context), in
  * the three steps of "What is the Mamba model?" (velog, Texnee), "chunkscan",

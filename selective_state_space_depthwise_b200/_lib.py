@@ -33,6 +33,13 @@ EXPORTED = (
     "ssm_proj_gemm",
     "ssm_proj_gemm_workspace_bytes",
     "ssm_ssd_chunk_scan",
+    "ssm_delta_prefill",
+    "ssm_delta_prefill_workspace_bytes",
+    "ssm_delta_decode_step",
+    "ssm_gated_norm",
+    "ssm_residual_norm",
+    "ssm_residual_block_forward",
+    "ssm_residual_block_workspace_bytes",
     "ssm_segment_summary",
     "ssm_segment_summary_workspace_bytes",
     "ssm_segment_carry",
@@ -92,6 +99,32 @@ class SsmSsdDims(ctypes.Structure):
                                              "chunk_size")]
 
 
+class SsmDeltaDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "ngroups", "d_key", "d_value")] + [
+        ("scale", ctypes.c_float), ("qk_l2norm", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in (
+            "q_tok_stride", "q_seq_stride", "k_tok_stride", "k_seq_stride", "v_tok_stride", "v_seq_stride",
+            "out_tok_stride", "out_seq_stride", "gb_tok_stride", "gb_seq_stride")]
+
+
+class SsmGatedNormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "dim", "group")] + [
+        ("eps", ctypes.c_float)] + [(n, ctypes.c_int32) for n in ("io_dtype", "gate_first", "shared_weight")] + [
+            (n, ctypes.c_int64) for n in ("x_tok_stride", "x_seq_stride", "z_tok_stride", "z_seq_stride",
+                                          "y_tok_stride", "y_seq_stride")]
+
+
+class SsmResidualNormDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("io_dtype", ctypes.c_int32),
+                ("residual_dtype", ctypes.c_int32)] + [(n, ctypes.c_int64) for n in (
+                    "x_stride", "residual_in_stride", "y_stride", "residual_out_stride")]
+
+
+class SsmBlockNorm(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("post_w", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("residual_dtype", ctypes.c_int32)]
+
+
 class SsmWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("conv_w", "conv_b", "w_dt", "dt_bias", "A_log", "D")]
 
@@ -145,6 +178,21 @@ def load(path: str = LIB_PATH):
     lib.ssm_proj_gemm_workspace_bytes.restype = sz
     lib.ssm_ssd_chunk_scan.argtypes = [ctypes.POINTER(SsmSsdDims)] + [p] * 8 + [p]
     lib.ssm_ssd_chunk_scan.restype = st
+    delta_p, bnorm_p = ctypes.POINTER(SsmDeltaDims), ctypes.POINTER(SsmBlockNorm)
+    lib.ssm_delta_prefill.argtypes = [delta_p] + [p] * 9 + [p, sz, p]
+    lib.ssm_delta_prefill.restype = st
+    lib.ssm_delta_prefill_workspace_bytes.argtypes = [delta_p]
+    lib.ssm_delta_prefill_workspace_bytes.restype = sz
+    lib.ssm_delta_decode_step.argtypes = [delta_p] + [p] * 6 + [i64] + [p] * 3 + [p]
+    lib.ssm_delta_decode_step.restype = st
+    lib.ssm_gated_norm.argtypes = [ctypes.POINTER(SsmGatedNormDims)] + [p] * 4 + [p]
+    lib.ssm_gated_norm.restype = st
+    lib.ssm_residual_norm.argtypes = [ctypes.POINTER(SsmResidualNormDims)] + [p] * 6 + [p]
+    lib.ssm_residual_norm.restype = st
+    lib.ssm_residual_block_forward.argtypes = [bdims_p, w_p, bw_p, bnorm_p] + [p] * 8 + [p, sz, p]
+    lib.ssm_residual_block_forward.restype = st
+    lib.ssm_residual_block_workspace_bytes.argtypes = [bdims_p]
+    lib.ssm_residual_block_workspace_bytes.restype = sz
     lib.ssm_segment_summary.argtypes = [dims_p, w_p] + [p] * 6 + [sz, p]
     lib.ssm_segment_summary.restype = st
     lib.ssm_segment_summary_workspace_bytes.argtypes = [dims_p]

@@ -395,6 +395,312 @@ def ssd_chunk_scan(cb, x, dt, dA_cumsum, C, prev_states, D=None, *, out=None, st
     return out
 
 
+def _device_stream(device, stream):
+    """The stream of the call on `device`: the one given, or that device's current stream. The tensors' device must
+    be the current one, on which the kernel is launched."""
+    if device.index is not None and device.index != torch.cuda.current_device():
+        raise RuntimeError(f"tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}: "
+                           "make the call under torch.cuda.device(...)")
+    return _stream(stream)
+
+
+def _stride(name, t, i):
+    """t's stride along dimension i for the C call: 0 (the dense default) where there is one index or none; an
+    expanded dimension has no stride that the call could express."""
+    if t.shape[i] <= 1 or not t.numel():
+        return 0
+    if t.stride(i) == 0:
+        raise ValueError(f"{name} is expanded along dimension {i}: make it contiguous")
+    return t.stride(i)
+
+
+def _row_stride(name, t):
+    """The one stride between the rows of t [rows, dim] or [b, L, dim]."""
+    if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if t.dim() == 2:
+        return _stride(name, t, 0)
+    s0, s1 = _stride(name, t, 0), _stride(name, t, 1)
+    if s0 and s1 and s0 != t.shape[1] * s1:
+        raise ValueError(f"the rows of {name} must be at one stride")
+    return s1 or s0
+
+
+def _dense_heads(name, t):
+    """The last two dimensions (head, channel) dense."""
+    if t.numel() and ((t.shape[-1] > 1 and t.stride(-1) != 1) or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1])):
+        raise ValueError(f"the head and channel dimensions of {name} must be contiguous")
+
+
+def _delta_dims(q, k, v, g, beta, scale, qk_l2norm, lead):
+    """Checks the token tensors of the delta rule ([*lead, heads, channels]; g, beta [*lead, heads]) and fills the
+    shape part of SsmDeltaDims."""
+    n = len(lead)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need_cuda(name, t, q.device)
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bfloat16")
+        if t.dim() != n + 2 or t.shape[:n] != lead:
+            raise ValueError(f"{name} must have shape [{'b, L' if n == 2 else 'tokens'}, heads, channels]")
+        _dense_heads(name, t)
+    H, G = v.shape[-2], q.shape[-2]
+    if k.shape != q.shape or G == 0 or H % G:
+        raise ValueError("k must have q's shape, and v's heads must be a multiple of q's")
+    for name, t in (("g", g), ("beta", beta)):
+        _need_cuda(name, t, q.device)
+        if t.dtype != torch.float32 or t.shape != lead + (H,) or (t.numel() and H > 1 and t.stride(-1) != 1):
+            raise ValueError(f"{name} must be float32 with one value per token and head of v, heads contiguous")
+    if g.stride() != beta.stride():
+        raise ValueError("g and beta must share strides")
+    if scale is not None and not scale > 0:
+        raise ValueError("scale must be positive")
+    d = _lib.SsmDeltaDims()
+    d.nheads, d.ngroups, d.d_key, d.d_value = H, G, q.shape[-1], v.shape[-1]
+    d.scale, d.qk_l2norm = scale or 0.0, int(bool(qk_l2norm))
+    return d
+
+
+def _delta_state(name, t, n, dims, device):
+    _need_cuda(name, t, device)
+    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 4
+                          or t.shape[1:] != (dims.nheads, dims.d_value, dims.d_key)
+                          or (n is not None and t.shape[0] != n)):
+        raise ValueError(f"{name} must be a contiguous float32 [{'states' if n is None else n}, {dims.nheads}, "
+                         f"{dims.d_value}, {dims.d_key}] tensor")
+
+
+def delta_prefill_workspace_bytes(batch, seqlen, nheads, ngroups, d_key, d_value) -> int:
+    d = _lib.SsmDeltaDims(batch, seqlen, nheads, ngroups, d_key, d_value)
+    return int(_lib.load().ssm_delta_prefill_workspace_bytes(ctypes.byref(d)))
+
+
+def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=None, qk_l2norm=False, out=None,
+                  state_out=None, workspace=None, stream=None):
+    """Gated delta rule over whole sequences (ssm_delta_prefill): per head
+    S <- a S + beta (v - a S k) k^T with a = exp(g), out = scale S q. q, k
+    [b, L, G, dk], v [b, L, H, dv] bf16 (head h reads group h // (H // G)), g,
+    beta [b, L, H] fp32; the last two dimensions dense, token and sequence
+    strides as they are. With cu_seqlens (int32 [n + 1] on the device) the
+    tensors are packed, [T, ...], sequence i being rows cu_seqlens[i] to
+    cu_seqlens[i + 1]; rows of no sequence keep what `out` held. state_in
+    [n, H, dv, dk] fp32 or None = zeros; scale None = dk ** -0.5; qk_l2norm
+    normalises q and k inside. Returns (out, state_out)."""
+    lib = _lib.load()
+    lead = q.shape[:-2]
+    if len(lead) != (1 if cu_seqlens is not None else 2):
+        raise ValueError("q must be [b, L, G, dk], or [tokens, G, dk] with cu_seqlens")
+    dev = q.device
+    d = _delta_dims(q, k, v, g, beta, scale, qk_l2norm, lead)
+    if cu_seqlens is not None:
+        _need_cuda("cu_seqlens", cu_seqlens, dev)
+        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
+                or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be a contiguous int32 [sequences + 1] tensor")
+        d.batch, d.seqlen = cu_seqlens.numel() - 1, lead[0]
+    else:
+        d.batch, d.seqlen = lead
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    _need_cuda("out", out, dev)
+    if out.shape != v.shape or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bfloat16 with v's shape")
+    _dense_heads("out", out)
+    _delta_state("state_in", state_in, d.batch, d, dev)
+    if state_out is None:
+        state_out = torch.empty((d.batch, d.nheads, d.d_value, d.d_key), dtype=torch.float32, device=dev)
+    _delta_state("state_out", state_out, d.batch, d, dev)
+    d.q_tok_stride, d.k_tok_stride, d.v_tok_stride = _stride("q", q, -3), _stride("k", k, -3), _stride("v", v, -3)
+    d.out_tok_stride, d.gb_tok_stride = _stride("out", out, -3), _stride("g", g, -2)
+    if cu_seqlens is None:
+        d.q_seq_stride, d.k_seq_stride, d.v_seq_stride = _stride("q", q, 0), _stride("k", k, 0), _stride("v", v, 0)
+        d.out_seq_stride, d.gb_seq_stride = _stride("out", out, 0), _stride("g", g, 0)
+    ws = int(lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(d)))
+    if ws and (workspace is None or workspace.numel() * workspace.element_size() < ws):
+        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    _need_cuda("workspace", workspace, dev)
+    _lib.check(lib.ssm_delta_prefill(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                     _ptr(cu_seqlens), _ptr(state_in), _ptr(out), _ptr(state_out),
+                                     _ptr(workspace) if ws else None, ws, _device_stream(dev, stream)))
+    return out, state_out
+
+
+def delta_decode_step(q, k, v, g, beta, state, *, state_index=None, scale=None, qk_l2norm=False, out=None,
+                      state_out=None, stream=None):
+    """Gated delta rule over one token per sequence (ssm_delta_decode_step):
+    q, k [b, G, dk], v [b, H, dv] bf16, g, beta [b, H] fp32. `state`
+    [states, H, dv, dk] fp32 is updated in place, or read only where state_out
+    (another pool of its shape) is given. state_index (int32 [b]): the state of
+    each row, negative = padding, whose output and state are left alone; no two
+    rows may name the same state. Returns out [b, H, dv]."""
+    lib = _lib.load()
+    dev = q.device
+    d = _delta_dims(q, k, v, g, beta, scale, qk_l2norm, q.shape[:1])
+    d.batch, d.seqlen = q.shape[0], 1
+    if state_index is not None:
+        _need_cuda("state_index", state_index, dev)
+        if state_index.dtype != torch.int32 or state_index.shape != (d.batch,) or not state_index.is_contiguous():
+            raise ValueError("state_index must be a contiguous int32 [b] tensor")
+    _delta_state("state", state, None if state_index is not None else d.batch, d, dev)
+    if state_out is None:
+        state_out = state
+    _delta_state("state_out", state_out, state.shape[0], d, dev)
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    _need_cuda("out", out, dev)
+    if out.shape != v.shape or out.dtype != torch.bfloat16:
+        raise ValueError("out must be bfloat16 with v's shape")
+    _dense_heads("out", out)
+    d.q_seq_stride, d.k_seq_stride, d.v_seq_stride = _stride("q", q, 0), _stride("k", k, 0), _stride("v", v, 0)
+    d.out_seq_stride, d.gb_seq_stride = _stride("out", out, 0), _stride("g", g, 0)
+    _lib.check(lib.ssm_delta_decode_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                         _ptr(state_index), state.shape[0], _ptr(state), _ptr(out), _ptr(state_out),
+                                         _device_stream(dev, stream)))
+    return out
+
+
+def gated_norm(x, z, weight, *, group_size=None, eps=1e-5, gate_first=False, out=None, stream=None):
+    """The norm between a scan and out_proj, fused with its gate
+    (ssm_gated_norm): per group of group_size channels (None = the row),
+    x / rms(x) * weight * SiLU(z), or with gate_first t / rms(t) * weight with
+    t = x * SiLU(z). x, z [rows, dim] or [b, L, dim] (bf16 or fp32, last
+    dimension contiguous, other strides as they are), z None = no gate; weight
+    fp32 [dim], or [group_size] for every group alike. out may be x or z.
+    Returns out."""
+    lib = _lib.load()
+    dev = x.device
+    if x.dim() not in (2, 3) or x.dtype not in _DTYPES:
+        raise ValueError("x must be a float32 or bfloat16 [rows, dim] or [b, L, dim] tensor")
+    dim = x.shape[-1]
+    group = dim if group_size is None else int(group_size)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    for n, t in (("x", x), ("z", z), ("out", out)):
+        _need_cuda(n, t, dev)
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or (t.numel() and dim > 1 and t.stride(-1) != 1)):
+            raise ValueError(f"{n} must have x's shape and dtype and a contiguous last dimension")
+    _need_cuda("weight", weight, dev)
+    if weight.dtype != torch.float32 or not weight.is_contiguous() or weight.shape not in ((dim,), (group,)):
+        raise ValueError("weight must be contiguous float32 [dim] or [group_size]")
+    d = _lib.SsmGatedNormDims()
+    d.batch, d.seqlen = (1, x.shape[0]) if x.dim() == 2 else x.shape[:2]
+    d.dim, d.group, d.eps, d.io_dtype = dim, group, eps, _DTYPES[x.dtype]
+    d.gate_first, d.shared_weight = int(bool(gate_first)), int(weight.shape[0] != dim)
+    d.x_tok_stride, d.y_tok_stride = _stride("x", x, -2), _stride("out", out, -2)
+    d.z_tok_stride = 0 if z is None else _stride("z", z, -2)
+    if x.dim() == 3:
+        d.x_seq_stride, d.y_seq_stride = _stride("x", x, 0), _stride("out", out, 0)
+        d.z_seq_stride = 0 if z is None else _stride("z", z, 0)
+    _lib.check(lib.ssm_gated_norm(ctypes.byref(d), _ptr(x), _ptr(z), _ptr(weight), _ptr(out),
+                                  _device_stream(dev, stream)))
+    return out
+
+
+def residual_norm(x, residual, weight, *, post_weight=None, residual_scale=1.0, eps=1e-5, out=None,
+                  residual_out=None, residual_dtype=None, stream=None):
+    """The step between two blocks in one pass (ssm_residual_norm): with
+    t = x, or x / rms(x) * post_weight, r = residual + residual_scale * t and
+    out = r / rms(r) * weight. x [rows, dim] or [b, L, dim] (bf16 or fp32, rows
+    at one stride), residual of x's shape (bf16 or fp32) or None = zeros (the
+    first block; residual_dtype then picks r's type, default x's); weights fp32
+    [dim]. residual_out may be residual. Returns (out, residual_out)."""
+    lib = _lib.load()
+    dev = x.device
+    if x.dim() not in (2, 3) or x.dtype not in _DTYPES:
+        raise ValueError("x must be a float32 or bfloat16 [rows, dim] or [b, L, dim] tensor")
+    dim = x.shape[-1]
+    rdt = residual.dtype if residual is not None else residual_dtype or (
+        residual_out.dtype if residual_out is not None else x.dtype)
+    if rdt not in _DTYPES or (residual_dtype is not None and residual_dtype != rdt):
+        raise ValueError("the residual must be float32 or bfloat16, of residual_dtype where that is given")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=rdt, device=dev)
+    d = _lib.SsmResidualNormDims()
+    for n, t, dt in (("x", x, x.dtype), ("residual", residual, rdt), ("out", out, x.dtype),
+                     ("residual_out", residual_out, rdt)):
+        _need_cuda(n, t, dev)
+        if t is None:
+            continue
+        if t.shape != x.shape or t.dtype != dt:
+            raise ValueError(f"{n} must be a {dt} tensor of x's shape")
+    for n, t in (("weight", weight), ("post_weight", post_weight)):
+        _need_cuda(n, t, dev)
+        if t is not None and (t.dtype != torch.float32 or t.shape != (dim,) or not t.is_contiguous()):
+            raise ValueError(f"{n} must be contiguous float32 [dim]")
+    d.rows, d.dim, d.eps, d.residual_scale = x.numel() // max(dim, 1), dim, eps, residual_scale
+    d.io_dtype, d.residual_dtype = _DTYPES[x.dtype], _DTYPES[rdt]
+    d.x_stride, d.y_stride, d.residual_out_stride = (_row_stride("x", x), _row_stride("out", out),
+                                                     _row_stride("residual_out", residual_out))
+    d.residual_in_stride = 0 if residual is None else _row_stride("residual", residual)
+    _lib.check(lib.ssm_residual_norm(ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), _ptr(post_weight),
+                                     _ptr(out), _ptr(residual_out), _device_stream(dev, stream)))
+    return out, residual_out
+
+
+def residual_block_workspace_bytes(batch, seqlen, d_model, E) -> int:
+    lib = _lib.load()
+    return int(lib.ssm_residual_block_workspace_bytes(ctypes.byref(make_block_dims(batch, seqlen, d_model, E))))
+
+
+def residual_block_forward(x, residual, params, proj, norm_weight, *, post_weight=None, residual_scale=1.0, eps=1e-5,
+                           residual_dtype=torch.float32, residual_out=None, conv_cache_in=None, ssm_state_in=None,
+                           out=None, conv_cache_out=None, ssm_state_out=None, dt_min=1e-4, dt_max=1.0,
+                           discretization="euler", workspace=None, stream=None):
+    """One pre-norm residual layer around the block (ssm_residual_block_forward):
+    (hidden, r) = residual_norm(x, residual, norm_weight, ...), out =
+    block_forward(hidden). x [b, L, D] bf16 is the previous block's output (or
+    the embedding, with residual None), contiguous; residual and r [b, L, D] in
+    residual_dtype, contiguous. The next layer takes (out, r). Returns (out, r,
+    conv_cache_out, ssm_state_out)."""
+    lib = _lib.load()
+    b, L, Dm = x.shape
+    dev = x.device
+    E = proj["W_x"].shape[1]
+    if residual is not None:
+        residual_dtype = residual.dtype
+    if residual_dtype not in _DTYPES:
+        raise ValueError("the residual must be float32 or bfloat16")
+    if residual_out is None:
+        residual_out = torch.empty((b, L, Dm), dtype=residual_dtype, device=dev)
+    if out is None:
+        out = torch.empty((b, L, Dm), dtype=torch.bfloat16, device=dev)
+    if conv_cache_out is None:
+        conv_cache_out = torch.empty((b, 3, E), dtype=torch.bfloat16, device=dev)
+    if ssm_state_out is None:
+        ssm_state_out = torch.empty((b, E, 16), dtype=torch.float32, device=dev)
+    full, cache, state = (b, L, Dm), (b, 3, E), (b, E, 16)
+    for n, t, shape, dt in (("x", x, full, torch.bfloat16), ("residual", residual, full, residual_dtype),
+                            ("residual_out", residual_out, full, residual_dtype), ("out", out, full, torch.bfloat16),
+                            ("W_in", proj["W_in"], (2 * E, Dm), torch.bfloat16),
+                            ("W_x", proj["W_x"], (33, E), torch.bfloat16),
+                            ("W_out", proj["W_out"], (Dm, E), torch.bfloat16),
+                            ("norm_weight", norm_weight, (Dm,), torch.float32),
+                            ("post_weight", post_weight, (Dm,), torch.float32),
+                            ("conv_cache_in", conv_cache_in, cache, torch.bfloat16),
+                            ("conv_cache_out", conv_cache_out, cache, torch.bfloat16),
+                            ("ssm_state_in", ssm_state_in, state, torch.float32),
+                            ("ssm_state_out", ssm_state_out, state, torch.float32)):
+        _need_cuda(n, t, dev)
+        if t is not None and (t.shape != shape or t.dtype != dt or not t.is_contiguous()):
+            raise ValueError(f"{n} must be a contiguous {dt} tensor of shape {shape}")
+    dims = make_block_dims(b, L, Dm, E, dt_min, dt_max, discretization)
+    w = _weights(params, E, dev)
+    pw = _lib.SsmBlockWeights(proj["W_in"].data_ptr(), proj["W_x"].data_ptr(), proj["W_out"].data_ptr())
+    nw = _lib.SsmBlockNorm(norm_weight.data_ptr(), None if post_weight is None else post_weight.data_ptr(), eps,
+                           residual_scale, _DTYPES[residual_dtype])
+    ws = int(lib.ssm_residual_block_workspace_bytes(ctypes.byref(dims)))
+    if workspace is None or workspace.numel() * workspace.element_size() < ws:
+        workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+    _need_cuda("workspace", workspace, dev)
+    _lib.check(lib.ssm_residual_block_forward(
+        ctypes.byref(dims), ctypes.byref(w), ctypes.byref(pw), ctypes.byref(nw), _ptr(x), _ptr(residual),
+        _ptr(conv_cache_in), _ptr(ssm_state_in), _ptr(residual_out), _ptr(out), _ptr(conv_cache_out),
+        _ptr(ssm_state_out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _device_stream(dev, stream)))
+    return out, residual_out, conv_cache_out, ssm_state_out
+
+
 def decode_step(x, z, B, C, dt_raw, params, conv_cache, ssm_state, *, y=None, dt_min=1e-4, dt_max=1.0,
                 discretization="euler", stream=None):
     """One-token block core. x, z: [b, E] (last dim contiguous); B, C: [b, 16];

@@ -477,4 +477,49 @@ ssm_status ssm_block_forward(const ssm_block_dims* dims, const ssm_weights* w, c
   return ssm::fail(SSM_OK, "");
 }
 
+size_t ssm_residual_block_workspace_bytes(const ssm_block_dims* dims) {
+  if (ssm::check_block_dims(dims) != SSM_OK) return 0;
+  const size_t hidden = static_cast<size_t>(dims->batch * dims->seqlen) * static_cast<size_t>(dims->d_model) * 2;
+  return ssm::block_layout(dims).bytes + ssm::align_up(hidden);
+}
+
+// The block's workspace, then the normed hidden rows [b L][D] bf16.
+ssm_status ssm_residual_block_forward(const ssm_block_dims* dims, const ssm_weights* w, const ssm_block_weights* proj,
+                                      const ssm_block_norm* norm, const void* x, const void* residual_in,
+                                      const void* conv_cache_in, const float* ssm_state_in, void* residual_out,
+                                      void* out, void* conv_cache_out, float* ssm_state_out, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  using ssm::fail;
+  ssm_status st = ssm::check_block_dims(dims);
+  if (st != SSM_OK) return st;
+  if (!norm) return fail(SSM_ERR_INVALID_ARG, "norm is NULL");
+  const ssm::BlockLayout lay = ssm::block_layout(dims);
+  void* hidden = nullptr;
+  if (dims->seqlen > 0) {
+    // everything the two calls below could refuse is refused before either runs
+    if ((st = ssm::check_weights(w)) != SSM_OK) return st;
+    if ((st = ssm::check_prefill_caches(conv_cache_in, ssm_state_in, conv_cache_out, ssm_state_out)) != SSM_OK)
+      return st;
+    if (!proj || !proj->w_in || !proj->w_x || !proj->w_out || !ssm::aligned(proj->w_in, 16) ||
+        !ssm::aligned(proj->w_x, 16) || !ssm::aligned(proj->w_out, 16))
+      return fail(SSM_ERR_INVALID_ARG, "proj or one of its weights is NULL or misaligned");
+    if (!out || !ssm::aligned(out, 16)) return fail(SSM_ERR_INVALID_ARG, "out is NULL or misaligned");
+    if (!residual_out) return fail(SSM_ERR_INVALID_ARG, "residual_out is NULL");
+    if (out == residual_out || out == residual_in)
+      return fail(SSM_ERR_INVALID_ARG, "out must not alias residual_in or residual_out");
+    const size_t need = ssm_residual_block_workspace_bytes(dims);
+    if (!workspace || !ssm::aligned(workspace, ssm::kAlign) || workspace_bytes < need)
+      return fail(SSM_ERR_INVALID_ARG, "workspace: need %zu bytes, %zu-byte aligned", need, ssm::kAlign);
+    hidden = static_cast<char*>(workspace) + lay.bytes;
+    ssm_residual_norm_dims nd{};
+    nd.rows = dims->batch * dims->seqlen, nd.dim = dims->d_model;
+    nd.eps = norm->eps, nd.residual_scale = norm->residual_scale;
+    nd.io_dtype = SSM_BF16, nd.residual_dtype = norm->residual_dtype;
+    if ((st = ssm_residual_norm(&nd, x, residual_in, norm->w, norm->post_w, hidden, residual_out, stream)) != SSM_OK)
+      return st;
+  }
+  return ssm_block_forward(dims, w, proj, hidden, conv_cache_in, ssm_state_in, out, conv_cache_out, ssm_state_out,
+                           workspace, lay.bytes, stream);
+}
+
 }  // extern "C"

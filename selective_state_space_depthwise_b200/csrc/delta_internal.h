@@ -1,0 +1,28 @@
+// delta_internal.h -- launch interface between the gated delta rule's entry
+// points (delta.cu) and its kernels (delta.cu, delta_chunk.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ssm {
+
+struct DeltaArgs {
+  const __nv_bfloat16 *q, *k, *v;
+  const float *g, *beta;
+  const int32_t* cu;     // packed sequences: [batch + 1] first rows, or null
+  const int32_t* index;  // decode: state of each row, or null
+  const float* state_in;
+  __nv_bfloat16* out;
+  float* state_out;
+  int64_t batch, L, H, G, dk, dv, num_states;
+  int64_t q_tok, q_seq, k_tok, k_seq, v_tok, v_seq, o_tok, o_seq, gb_tok, gb_seq;
+  float scale;
+  int l2norm;
+  int* err;
+};
+
+constexpr float kL2Eps = 1e-6f;
+
+}  // namespace ssm
