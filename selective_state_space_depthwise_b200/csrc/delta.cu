@@ -27,6 +27,7 @@
 namespace ssm {
 namespace {
 
+constexpr int kChunkFrom = 20;  // tokens from which a sequence goes to the chunk kernel
 constexpr int kRecWarps = 4;
 constexpr int kRecSteps = 8;  // row steps of a warp
 
@@ -249,7 +250,15 @@ ssm_status ssm_delta_prefill(const ssm_delta_dims* dims, const void* q, const vo
   if (st != SSM_OK) return st;
   if (cu_seqlens && !ssm::aligned(cu_seqlens, 4)) return fail(SSM_ERR_INVALID_ARG, "cu_seqlens is not 4-byte aligned");
   a.cu = cu_seqlens;
-  const cudaError_t err = ssm::launch_delta_recurrent(a, static_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  if (a.L > 0 && (a.cu || a.L >= ssm::kChunkFrom)) {
+    a.err = ssm::device_error_ptr();
+    if (!a.err) return fail(SSM_ERR_CUDA, "device error word: %s", cudaGetErrorString(cudaGetLastError()));
+    err = ssm::launch_delta_chunk(a, cs);
+  } else {
+    err = ssm::launch_delta_recurrent(a, cs);
+  }
   if (err != cudaSuccess) return fail(SSM_ERR_CUDA, "delta-rule launch: %s", cudaGetErrorString(err));
   return fail(SSM_OK, "");
 }

@@ -23,6 +23,9 @@ struct DeltaArgs {
   int* err;
 };
 
+// 64 tokens at a time on the tensor cores; a.L > 0.
+cudaError_t launch_delta_chunk(const DeltaArgs& a, cudaStream_t st);
+
 constexpr float kL2Eps = 1e-6f;
 
 }  // namespace ssm
