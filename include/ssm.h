@@ -465,13 +465,15 @@ typedef struct {
  *   out         [b, L, nheads, d_value] bf16; must not overlap the inputs
  *   state_out   [b, nheads, d_value, d_key] fp32, dense: the state after the
  *               last token; may be state_in
- *   workspace   ssm_delta_prefill_workspace_bytes(dims) bytes of device
- *               scratch, 256-byte aligned, or NULL when that is 0. Calls that
- *               overlap on the GPU need separate workspaces.
+ *   workspace   ssm_delta_prefill_workspace_bytes() bytes of device scratch,
+ *               256-byte aligned, or NULL when that is 0 (26 KB for each 64
+ *               tokens and head, plus as much for each packed sequence). Calls
+ *               that overlap on the GPU need separate workspaces.
  * A long sequence may be processed in pieces: feeding one call's state_out to
  * the next gives the result of one call up to fp32 rounding.
  */
-size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims *dims);
+/* Workspace of a call with these dims, with (packed = 1) or without cu_seqlens; 0 for invalid dims. */
+size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims *dims, int32_t packed);
 ssm_status ssm_delta_prefill(const ssm_delta_dims *dims, const void *q, const void *k, const void *v, const float *g,
                              const float *beta, const int32_t *cu_seqlens, const float *state_in, void *out,
                              float *state_out, void *workspace, size_t workspace_bytes, void *stream);

@@ -181,7 +181,7 @@ def load(path: str = LIB_PATH):
     delta_p, bnorm_p = ctypes.POINTER(SsmDeltaDims), ctypes.POINTER(SsmBlockNorm)
     lib.ssm_delta_prefill.argtypes = [delta_p] + [p] * 9 + [p, sz, p]
     lib.ssm_delta_prefill.restype = st
-    lib.ssm_delta_prefill_workspace_bytes.argtypes = [delta_p]
+    lib.ssm_delta_prefill_workspace_bytes.argtypes = [delta_p, ctypes.c_int32]
     lib.ssm_delta_prefill_workspace_bytes.restype = sz
     lib.ssm_delta_decode_step.argtypes = [delta_p] + [p] * 6 + [i64] + [p] * 3 + [p]
     lib.ssm_delta_decode_step.restype = st

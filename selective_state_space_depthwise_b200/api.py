@@ -469,9 +469,10 @@ def _delta_state(name, t, n, dims, device):
                          f"{dims.d_value}, {dims.d_key}] tensor")
 
 
-def delta_prefill_workspace_bytes(batch, seqlen, nheads, ngroups, d_key, d_value) -> int:
+def delta_prefill_workspace_bytes(batch, seqlen, nheads, ngroups, d_key, d_value, packed=False) -> int:
+    """Workspace bytes of `delta_prefill`; with packed, for `batch` sequences in a buffer of `seqlen` tokens."""
     d = _lib.SsmDeltaDims(batch, seqlen, nheads, ngroups, d_key, d_value)
-    return int(_lib.load().ssm_delta_prefill_workspace_bytes(ctypes.byref(d)))
+    return int(_lib.load().ssm_delta_prefill_workspace_bytes(ctypes.byref(d), int(bool(packed))))
 
 
 def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=None, qk_l2norm=False, out=None,
@@ -514,7 +515,7 @@ def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=Non
     if cu_seqlens is None:
         d.q_seq_stride, d.k_seq_stride, d.v_seq_stride = _stride("q", q, 0), _stride("k", k, 0), _stride("v", v, 0)
         d.out_seq_stride, d.gb_seq_stride = _stride("out", out, 0), _stride("g", g, 0)
-    ws = int(lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(d)))
+    ws = int(lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(d), int(cu_seqlens is not None)))
     if ws and (workspace is None or workspace.numel() * workspace.element_size() < ws):
         workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
     _need_cuda("workspace", workspace, dev)

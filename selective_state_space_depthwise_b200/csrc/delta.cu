@@ -169,10 +169,7 @@ cudaError_t launch_delta_recurrent(const DeltaArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Shape, stride and pointer checks shared by both entry points.
-ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, const void* k, const void* v,
-                      const float* g, const float* beta, void* out, const float* state_in, float* state_out,
-                      DeltaArgs* a) {
+ssm_status delta_shape(const ssm_delta_dims* d, bool prefill) {
   if (!d) return fail(SSM_ERR_INVALID_ARG, "dims is NULL");
   if (d->batch <= 0) return fail(SSM_ERR_INVALID_ARG, "batch=%lld must be > 0", (long long)d->batch);
   if (prefill && (d->seqlen < 0 || d->seqlen > 0x7fffff00))
@@ -184,10 +181,24 @@ ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, cons
     return fail(SSM_ERR_UNSUPPORTED, "d_key=%lld: built for multiples of 8 up to 128", (long long)d->d_key);
   if (d->d_value < 8 || d->d_value > 4096 || d->d_value % 8 != 0)
     return fail(SSM_ERR_UNSUPPORTED, "d_value=%lld: built for multiples of 8 up to 4096", (long long)d->d_value);
-  if (d->batch > 0x7fffffff / 256 / d->nheads)
+  if (d->nheads > 0x7fffff || d->batch > 0x7fffff / d->nheads)
     return fail(SSM_ERR_INVALID_ARG, "batch * nheads must be below 2^23");
+  if (prefill && d->seqlen > 0 && d->seqlen / 64 + 1 > 0x7fffffff / (d->batch * d->nheads))
+    return fail(SSM_ERR_INVALID_ARG, "batch * nheads * seqlen / 64 must be below 2^31");
   if (!(d->scale >= 0.0f)) return fail(SSM_ERR_INVALID_ARG, "scale=%g must be > 0, or 0 for the default", d->scale);
   if (d->qk_l2norm != 0 && d->qk_l2norm != 1) return fail(SSM_ERR_INVALID_ARG, "qk_l2norm must be 0 or 1");
+  return SSM_OK;
+}
+
+// Whether a prefill takes the chunk kernels. Packed lengths are known on the device alone.
+bool takes_chunks(int64_t L, bool packed) { return L > 0 && (packed || L >= kChunkFrom); }
+
+// Shape, stride and pointer checks shared by both entry points.
+ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, const void* k, const void* v,
+                      const float* g, const float* beta, void* out, const float* state_in, float* state_out,
+                      DeltaArgs* a) {
+  const ssm_status shape = delta_shape(d, prefill);
+  if (shape != SSM_OK) return shape;
   const int64_t L = prefill ? d->seqlen : 1, nk = d->ngroups * d->d_key, nv = d->nheads * d->d_value;
   a->batch = d->batch, a->L = L, a->H = d->nheads, a->G = d->ngroups, a->dk = d->d_key, a->dv = d->d_value;
   auto tok = [](int64_t given, int64_t dense) { return given ? given : dense; };
@@ -235,16 +246,15 @@ ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, cons
 
 extern "C" {
 
-size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims* dims) {
-  (void)dims;
-  return 0;
+size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims* dims, int32_t packed) {
+  if (ssm::delta_shape(dims, true) != SSM_OK || !ssm::takes_chunks(dims->seqlen, packed)) return 0;
+  return ssm::delta_chunk_workspace(dims->batch, dims->seqlen, dims->nheads, packed);
 }
 
 ssm_status ssm_delta_prefill(const ssm_delta_dims* dims, const void* q, const void* k, const void* v, const float* g,
                              const float* beta, const int32_t* cu_seqlens, const float* state_in, void* out,
                              float* state_out, void* workspace, size_t workspace_bytes, void* stream) {
   using ssm::fail;
-  (void)workspace, (void)workspace_bytes;
   ssm::DeltaArgs a{};
   const ssm_status st = ssm::delta_args(dims, true, q, k, v, g, beta, out, state_in, state_out, &a);
   if (st != SSM_OK) return st;
@@ -252,10 +262,15 @@ ssm_status ssm_delta_prefill(const ssm_delta_dims* dims, const void* q, const vo
   a.cu = cu_seqlens;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t err;
-  if (a.L > 0 && (a.cu || a.L >= ssm::kChunkFrom)) {
+  if (ssm::takes_chunks(a.L, a.cu)) {
+    const size_t need = ssm::delta_chunk_workspace(a.batch, a.L, a.H, a.cu);
+    if (!workspace || !ssm::aligned(workspace, 256))
+      return fail(SSM_ERR_INVALID_ARG, "workspace is NULL or not 256-byte aligned");
+    if (workspace_bytes < need)
+      return fail(SSM_ERR_INVALID_ARG, "workspace of %zu bytes, need %zu", workspace_bytes, need);
     a.err = ssm::device_error_ptr();
     if (!a.err) return fail(SSM_ERR_CUDA, "device error word: %s", cudaGetErrorString(cudaGetLastError()));
-    err = ssm::launch_delta_chunk(a, cs);
+    err = ssm::launch_delta_chunk(a, workspace, cs);
   } else {
     err = ssm::launch_delta_recurrent(a, cs);
   }

@@ -7,18 +7,26 @@
 //   (I + A) U = diag(beta) (V - diag(e^G) K S^T),
 //   A_ij = beta_i e^{G_i - G_j} k_i.k_j   (j < i),
 //
-// so with T = (I + A)^-1 diag(beta), a unit triangular inverse that does not
-// depend on S, a chunk is four products around the state:
+// so with T = (I + A)^-1 diag(beta), which does not depend on S, a chunk is
+// four products around the state:
 //
 //   Y = K S^T,  R = V - diag(e^G) Y,  U = T R,
 //   O = scale (diag(e^G) Q S^T + (Q K^T * e^{G_i - G_j}, j <= i) U),
 //   S <- e^{G_C} S + sum_j e^{G_C - G_j} u_j k_j^T.
 //
-// Transposed, with the 128 rows of S (a slice of d_value) as the 128 lanes of
-// tensor memory, every left operand (S, R, U) is an accumulator read back,
-// scaled and split in registers, and stored to tensor memory as the next
+// Two kernels. What does not depend on S (T, the masked scores and the decay
+// factors) is formed for all chunks at once by delta_prep_kernel and left in
+// the workspace as the operand tiles that the second kernel's products read
+// (26 KB per chunk and head). delta_chain_kernel then walks the chunks of a
+// sequence. (One kernel with warps that prepare the next chunk beside those
+// that walk took 10.9 us a chunk: the preparation alone is 2/3 of the
+// instructions, and waits for nothing but the walk's place on the SM.)
+//
+// The walk. Transposed, with the 128 rows of S (a slice of d_value) as the 128
+// lanes of tensor memory, every left operand (S, R, U) is an accumulator read
+// back, scaled and split in registers, and stored to tensor memory as the next
 // product's A operand: the state never leaves the SM, and shared memory holds
-// only the right operands (K, Q by TMA; T and the masked scores).
+// only the right operands (K, Q, T and the scores, by TMA).
 //
 // Precision. q, k and v are bf16 and enter exactly; the key norms, decays and
 // beta are fp32 factors of rows and columns, never folded into a bf16 operand.
@@ -29,14 +37,6 @@
 // fp32 accumulators with truncation, so the state itself is added up in fp32
 // registers, and the accumulators hold one chunk's contribution at a time.
 //
-// One CTA per (sequence, head, 128 rows of d_value), 20 warps:
-//   warps 0-7   state: hold S (a thread: one row, half of the key channels),
-//               form the A operands between the products;
-//   warps 8-11  prep, one chunk ahead: running decays, key norms, A and the
-//               masked scores from one 128 x 64 product [K; Q] K^T, the inverse;
-//   warps 12-15 output: both terms of O from tensor memory, rounded and stored;
-//   warp 16     one thread issues the TMA loads (three chunks ahead) and every MMA
-//               (warps 17-19 only complete its warpgroup).
 // Values that are not finite: a product with a zero would spread them to tokens
 // before theirs, so the state warps take them out of the operands, mark the
 // first such token of each row, and the output warps write NaN from there on.
@@ -53,68 +53,60 @@
 namespace ssm {
 namespace {
 
-constexpr int kC = 64;  // tokens of a chunk
-constexpr int kStateWarps = 8, kPrepWarp = 8, kOutWarp = 12, kCtlWarp = 16;
-constexpr int kChunkThreads = 32 * 20;
-// Registers. 20 warps launch with 96 a thread (five warps on each quarter of
-// an SM); the state warps, which hold half a row of S, take what the output
-// and control warps give up: 2 x 120 + 96 + 88 + 56 = 5 x 96.
-constexpr int kLaunchRegs = 96, kStateRegs = 120, kOutRegs = 88, kCtlRegs = 56;
-static_assert(2 * kStateRegs + kLaunchRegs + kOutRegs + kCtlRegs <= 5 * kLaunchRegs, "register split");
-constexpr int kStages = 3;
-constexpr int kALd = 68;  // floats between rows of A (16-byte rows, conflict-free columns)
+constexpr int kC = 64;            // tokens of a chunk
+constexpr int kAtom = kC * 128;   // 64 rows of 64 bf16: one swizzled operand atom
 
-// Tensor memory, 512 columns.
-constexpr uint32_t kTmDelta = 0;    // the chunk's contribution to S; before it, R's three terms
-constexpr uint32_t kTmS = 128;      // S's three terms: half h at 96 h; then U's scaled terms in the second half
-constexpr uint32_t kTmY = 320;      // Y, then U
-constexpr uint32_t kTmO = 384;      // Q S^T, then the scores times U
-constexpr uint32_t kTmG = 448;      // [K; Q] K^T of the next chunk; then U's two output terms
-
+// What the walk needs of a chunk and head, as the prep kernel leaves it: T in
+// three terms and the scores in two, each as four panels of 16 columns j (the
+// K of one MMA) and the rows i from 16 kk on, K-major without swizzle (8 rows
+// x 16 bytes contiguous, the two halves of a panel's columns 128 bytes apart,
+// 8-row groups 256 bytes apart); then the factors.
+constexpr int kPanelTerm = (64 + 48 + 32 + 16) * 32;  // 5120 bytes of one term
+__host__ __device__ constexpr int panel_off(int kk) { return 32 * (64 * kk - 8 * kk * (kk - 1)); }
 struct Coef {
-  float eg[kC];   // e^{G_j} |k_j|^-1: scales Y
-  float ec[kC];   // e^{G_C - G_j} |k_j|^-1, 0 behind the sequence: scales U into the state
-  float oq[kC];   // scale e^{G_i} |q_i|^-1: scales Q S^T
-  float decay;    // e^{G_C}
+  float eg[kC];  // e^{G_j} / |k_j|: scales Y
+  float ec[kC];  // e^{G_C - G_j} / |k_j|, 0 behind the sequence: scales U into the state
+  float oq[kC];  // scale e^{G_i} / |q_i|: scales Q S^T
+  float decay;   // e^{G_C}
   float pad[3];
 };
+constexpr int kImgP = 3 * kPanelTerm, kImgCoef = 5 * kPanelTerm;
+constexpr int kImgBytes = kImgCoef + static_cast<int>(sizeof(Coef));
+constexpr int kImgStride = (kImgBytes + 127) / 128 * 128;
+static_assert(panel_off(1) == 2048 && panel_off(3) == 4608 && kImgBytes % 16 == 0, "panel layout");
 
-template <int KA>  // 64-column atoms of d_key
-struct ChunkSmem {
-  static constexpr int kAtom = kC * 128;          // 64 rows of 128 bytes
-  static constexpr int kKQ = KA * 2 * kAtom;      // per atom: K, then Q
-  static constexpr int kV = kC * 256;             // [token][128]
-  static constexpr int kStage = kKQ + kV;
-  static constexpr int kT = kStages * kStage;     // three terms [i][j]
-  static constexpr int kP = kT + 3 * kAtom;       // two buffers of two terms [i][j]
-  static constexpr int kA = kP + 4 * kAtom;       // fp32 [64][kALd]
-  static constexpr int kCoef = kA + kC * kALd * 4;
-  static constexpr int kVec = kCoef + 4 * static_cast<int>(sizeof(Coef));  // Ghi, Glo, rk [64], beta [2][64]
-  static constexpr int kBad = kVec + 5 * kC * 4;  // int [2][128]
-  static constexpr int kBar = kBad + 2 * 128 * 4;
-  static constexpr int kNumBars = kStages + 15;
-  static constexpr int kMisc = kBar + kNumBars * 8;  // TMEM address, abort flag
-  static constexpr int kTotal = kMisc + 16;
-  static_assert(kBar % 8 == 0 && kCoef % 16 == 0 && kVec % 16 == 0, "alignment");
-  static_assert(kTotal + 1024 <= 232448, "227 KB of shared memory");
-  static constexpr uint32_t kTx = static_cast<uint32_t>(kStage);
-};
+// 16-byte piece of row i, columns 8 j8 .. 8 j8 + 7 within a term's panels.
+__device__ __forceinline__ int panel_piece(int i, int j8) {
+  const int kk = j8 >> 1, r = i - 16 * kk;
+  return panel_off(kk) + (r >> 3) * 256 + (j8 & 1) * 128 + (r & 7) * 16;
+}
 
-enum Bar {  // after the stages' full barriers; each completes once a chunk
-  kGDone, kGFree, kTPReady, kSReady0, kSReady1, kYDone, kOiDone, kRReady, kUDone, kUsReady, kSDone0, kSDone1, kUoReady,
-  kOiRead, kOaDone,  // kOFree follows
-  kNumNamed
+// Sequence s in rows: first row and length, in the packed buffer or on its own.
+struct Span {
+  int t0, len, seq;
 };
-static_assert(kNumNamed == 15, "barrier count");
-
-struct ChunkMaps {
-  CUtensorMap q, k, v;
-};
+__device__ __forceinline__ Span span_of(const DeltaArgs& a, int s) {
+  if (!a.cu) return {0, static_cast<int>(a.L), s};
+  const int T = static_cast<int>(a.L);
+  const int t0 = min(max(a.cu[s], 0), T);
+  return {t0, min(max(a.cu[s + 1], t0), T) - t0, 0};
+}
+// The first workspace slot of sequence s (a slot per chunk and head): chunks
+// of sequences that follow one another in the buffer never share one.
+__device__ __forceinline__ int64_t slot_of(const DeltaArgs& a, int s, int t0) {
+  return a.cu ? t0 / kC + s : static_cast<int64_t>(s) * ((a.L + kC - 1) / kC);
+}
 
 __host__ __device__ constexpr uint32_t chunk_idesc(int n, bool b_mn_major) {  // bf16 x bf16 -> fp32, M = 128
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? (1u << 16) : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
          (8u << 24);
 }
+// Descriptor of a panel: K-major, no swizzle, 128 bytes between the halves of K, 256 between 8-row groups.
+__device__ __forceinline__ uint64_t panel_desc(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(128u >> 4) << 16) |
+         (static_cast<uint64_t>(256u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46);
+}
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
 // A wait that all threads of a warp make together. Once any wait of the CTA
 // has run out, the flag lets the others through: every loop ends, on memory
@@ -122,12 +114,11 @@ __host__ __device__ constexpr uint32_t chunk_idesc(int n, bool b_mn_major) {  //
 struct Waiter {
   volatile int* abort;
   int* err;
-  __device__ __forceinline__ void slow(uint32_t bar, uint32_t parity, int code) const {
+  __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity, int code) const {
+    if (mbar_try_wait(bar, parity)) return;
     const uint64_t t0 = globaltimer_ns();
-    for (;;) {
 #pragma unroll 1
-      for (int i = 0; i < 64; ++i)
-        if (mbar_try_wait(bar, parity)) return;
+    while (!mbar_try_wait(bar, parity)) {
       if (*abort) return;
       if (globaltimer_ns() - t0 > 2000000000ull) {
         *abort = 1;
@@ -136,34 +127,41 @@ struct Waiter {
       }
     }
   }
-  __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity, int code) const {
-    if (!mbar_try_wait(bar, parity)) slow(bar, parity, code);
-  }
 };
 
-// x0, x1 as three packed bf16 pairs whose sum is exact: 8 bits of the significand each.
-__device__ __forceinline__ void split3(float x0, float x1, uint32_t& h, uint32_t& m, uint32_t& l) {
-  const uint32_t a0 = __float_as_uint(x0), a1 = __float_as_uint(x1);
-  h = __byte_perm(a0, a1, 0x7632);
-  const float r0 = x0 - __uint_as_float(a0 & 0xffff0000u), r1 = x1 - __uint_as_float(a1 & 0xffff0000u);
-  const uint32_t b0 = __float_as_uint(r0), b1 = __float_as_uint(r1);
-  m = __byte_perm(b0, b1, 0x7632);
-  const float s0 = r0 - __uint_as_float(b0 & 0xffff0000u), s1 = r1 - __uint_as_float(b1 & 0xffff0000u);
-  l = __byte_perm(__float_as_uint(s0), __float_as_uint(s1), 0x7632);
+// A pair of values as three packed bf16 pairs whose sum is exact: 8 bits of the significand each.
+__device__ __forceinline__ void split3(uint64_t x, uint32_t& h, uint32_t& m, uint32_t& l) {
+  const uint64_t minus = pk2(-1.0f, -1.0f);
+  float a, b;
+  upk2(x, a, b);
+  h = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  const uint64_t r = ffma2(pk2(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(b) & 0xffff0000u)), minus, x);
+  upk2(r, a, b);
+  m = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  const uint64_t s = ffma2(pk2(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(b) & 0xffff0000u)), minus, r);
+  upk2(s, a, b);
+  l = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& h, uint32_t& m) {
-  const uint32_t a0 = __float_as_uint(x0), a1 = __float_as_uint(x1);
-  h = __byte_perm(a0, a1, 0x7632);
-  const float r0 = x0 - __uint_as_float(a0 & 0xffff0000u), r1 = x1 - __uint_as_float(a1 & 0xffff0000u);
-  const __nv_bfloat162 p = __floats2bfloat162_rn(r0, r1);
+// As two: the top 8 bits, and the rest rounded.
+__device__ __forceinline__ void split2(uint64_t x, uint32_t& h, uint32_t& m) {
+  float a, b;
+  upk2(x, a, b);
+  h = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  const uint64_t r = ffma2(pk2(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(b) & 0xffff0000u)), pk2(-1.0f, -1.0f), x);
+  upk2(r, a, b);
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
   m = *reinterpret_cast<const uint32_t*>(&p);
 }
+__device__ __forceinline__ uint64_t pk2u(uint32_t a, uint32_t b) { return pk2(__uint_as_float(a), __uint_as_float(b)); }
 
 // 16 values of a row as three terms at columns col + t * stride of A-operand tensor memory.
-__device__ __forceinline__ void store_split3(uint32_t col, uint32_t stride, const float (&x)[16]) {
+__device__ __forceinline__ void store_split3(uint32_t col, uint32_t stride, const uint64_t (&x)[8]) {
   uint32_t h[8], m[8], l[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) split3(x[2 * i], x[2 * i + 1], h[i], m[i], l[i]);
+  for (int i = 0; i < 8; ++i) split3(x[i], h[i], m[i], l[i]);
   tmem_st_x8(col, h);
   tmem_st_x8(col + stride, m);
   tmem_st_x8(col + 2 * stride, l);
@@ -171,26 +169,362 @@ __device__ __forceinline__ void store_split3(uint32_t col, uint32_t stride, cons
 
 __device__ __forceinline__ int sw128(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-// Bit i set where x[i] is not finite.
-template <int N>
-__device__ __forceinline__ uint32_t not_finite(const float (&x)[N]) {
-  float s = 0.0f;
+// Bit i set where value i of the 16 is not finite.
+__device__ __forceinline__ uint32_t not_finite(const uint64_t (&x)[8]) {
+  uint64_t s = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) s = fmaf(x[i], 0.0f, s);
-  if (s == 0.0f) return 0u;
+  for (int i = 0; i < 8; ++i) s = ffma2(x[i], 0ull, s);
+  float a, b;
+  upk2(s, a, b);
   uint32_t bits = 0;
+  if (!(a + b == 0.0f)) {
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (!(fabsf(x[i]) <= 3.4028235e38f)) bits |= 1u << i;
+    for (int i = 0; i < 8; ++i) {
+      upk2(x[i], a, b);
+      bits |= (fabsf(a) <= 3.4028235e38f ? 0u : 1u << (2 * i)) | (fabsf(b) <= 3.4028235e38f ? 0u : 2u << (2 * i));
+    }
+  }
+  __syncwarp();
   return bits;
 }
+// Puts `to` in the place of the marked ones.
+__device__ __forceinline__ void replace_marked(uint64_t (&x)[8], uint32_t marks, float to) {
+  if (marks) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      upk2(x[i], a, b);
+      x[i] = pk2(marks >> (2 * i) & 1 ? to : a, marks >> (2 * i + 1) & 1 ? to : b);
+    }
+  }
+  __syncwarp();
+}
 
-constexpr int kPrepBar = 1;  // named barrier of the prep warps
+struct ChunkMaps {
+  CUtensorMap q, k, v;
+};
+
+// ------------------------------------------------------------------- prep ---
+// One CTA of 4 warps per chunk and up to kPrepHeads heads of one key group,
+// four to an SM. Thread pt owns row pt of the 128 x 64 product [K; Q] K^T (one
+// set of MMAs per CTA; tensor memory keeps it for all its heads): rows 0-63
+// give A, rows 64-127 the scores. The inverse of I + A: the two 32 x 32
+// diagonal blocks by substitution, a column per thread; then the block below
+// them, -T22 (A21 T11), eight rows of a column per thread.
+constexpr int kPrepHeads = 4;
+constexpr int kALd = 68;  // floats between rows of A (16-byte rows, conflict-free columns)
+
+template <int KA>  // 64-column atoms of d_key
+struct PrepSmem {
+  // from 0, per atom: K, then Q
+  static constexpr int kA = KA * 2 * kAtom;
+  static constexpr int kVec = kA + kC * kALd * 4;  // Ghi, Glo, rk, beta [64]
+  static constexpr int kBar = kVec + 4 * kC * 4;
+  static constexpr int kTotal = kBar + 32;  // full, done, TMEM address, abort flag
+};
 
 template <int KA>
-__global__ void __launch_bounds__(kChunkThreads, 1)
-    delta_chunk_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, int slices) {
-  using M = ChunkSmem<KA>;
+__global__ void __launch_bounds__(128, 4)
+    delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int head_sets) {
+  using M = PrepSmem<KA>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int pt = threadIdx.x, lane = pt & 31;
+  const int warp = __shfl_sync(0xffffffffu, pt >> 5, 0);
+  const int rep = static_cast<int>(a.H / a.G);
+  const int set = static_cast<int>(blockIdx.x) % head_sets;
+  const int64_t gslot = blockIdx.x / head_sets;
+  const int grp = static_cast<int>(gslot % a.G);
+  const int64_t slot = gslot / a.G;
+  // the sequence and chunk of this slot
+  int s, c;
+  if (a.cu) {
+    int lo = 0, hi = static_cast<int>(a.batch) - 1;  // the last sequence whose first slot is not behind this one
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (slot_of(a, mid, span_of(a, mid).t0) <= slot) lo = mid;
+      else hi = mid - 1;
+    }
+    s = lo;
+    c = static_cast<int>(slot - slot_of(a, s, span_of(a, s).t0));
+  } else {
+    const int nc = static_cast<int>((a.L + kC - 1) / kC);
+    s = static_cast<int>(slot / nc), c = static_cast<int>(slot % nc);
+  }
+  const Span sp = span_of(a, s);
+  if (c < 0 || kC * c >= sp.len) return;
+  const int n = min(kC, sp.len - kC * c), tok = sp.t0 + kC * c;
+
+  const uint32_t full = sb + M::kBar, done = sb + M::kBar + 8;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + M::kBar + 20);
+  const Waiter wait{abort, a.err};
+  if (pt == 0) {
+    mbar_init(full, 1);
+    mbar_init(done, 1);
+    *abort = 0;
+    mbar_fence_init();
+    mbar_arrive_expect_tx(full, KA * 2 * kAtom);
+#pragma unroll
+    for (int t = 0; t < KA; ++t) {
+      tma_load_4d(sb + t * 2 * kAtom, &maps.k, 64 * t, grp, tok, sp.seq, full);
+      tma_load_4d(sb + t * 2 * kAtom + kAtom, &maps.q, 64 * t, grp, tok, sp.seq, full);
+    }
+  }
+  if (warp == 0) {
+    __syncwarp();
+    tmem_alloc(sb + M::kBar + 16, 64);
+    tmem_relinquish();
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + M::kBar + 16);
+  wait(full, 0, 31);
+  if (pt == 0) {
+#pragma unroll
+    for (int t = 0; t < KA; ++t)
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        const uint64_t d = umma_desc_k_sw128(sb + t * 2 * kAtom + 32 * kk);
+        umma_f16_ss(tmem, d, d, chunk_idesc(64, false), t + kk > 0);
+      }
+    umma_commit(done);
+  }
+  __syncwarp();
+
+  const int i = pt & 63;  // this row's token
+  const bool is_q = pt >= 64;
+  float* As = reinterpret_cast<float*>(smem + M::kA);
+  float* Ghi = reinterpret_cast<float*>(smem + M::kVec);
+  float* Glo = Ghi + kC;
+  float* rk = Glo + kC;
+  float* beta = rk + kC;
+  float rn = 1.0f;  // 1 / |row|
+  if (a.l2norm) {
+    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll 1
+    for (int t = 0; t < KA; ++t) {
+      const unsigned char* base = smem + t * 2 * kAtom + (is_q ? kAtom : 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 w = *reinterpret_cast<const uint4*>(base + sw128(i, j));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xffff0000u);
+          s0 = fmaf(lo, lo, s0), s1 = fmaf(hi, hi, s1);
+        }
+      }
+    }
+    rn = rsqrtf(s0 + s1 + kL2Eps);
+  }
+  if (!is_q) rk[i] = rn;
+  wait(done, 0, 32);
+  tcgen05_fence_after();
+
+  const int h0 = grp * rep + set * kPrepHeads, h1 = min(h0 + kPrepHeads, (grp + 1) * rep);
+  const int64_t gb0 = static_cast<int64_t>(sp.seq) * a.gb_seq + static_cast<int64_t>(tok) * a.gb_tok;
+#pragma unroll 1
+  for (int h = h0; h < h1; ++h) {
+    unsigned char* img = img0 + (slot * a.H + h) * kImgStride;
+    // Running sums of g in log2 units and fp64, kept as two floats: differences of far sums stay exact.
+    if (warp == 0) {
+      auto lg = [&](int j) {
+        const double v = j < n ? static_cast<double>(a.g[gb0 + j * a.gb_tok + h]) * 1.4426950408889634 : 0.0;
+        return v < -256.0 ? -256.0 : v;
+      };
+      const double g0 = lg(2 * lane), g1 = lg(2 * lane + 1);
+      double sum = g0 + g1;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const double o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const double first = sum - g1;
+      const float f0 = static_cast<float>(first), f1 = static_cast<float>(sum);
+      Ghi[2 * lane] = f0, Ghi[2 * lane + 1] = f1;
+      Glo[2 * lane] = static_cast<float>(first - f0), Glo[2 * lane + 1] = static_cast<float>(sum - f1);
+    } else if (is_q) {
+      beta[i] = i < n ? a.beta[gb0 + i * a.gb_tok + h] : 0.0f;
+    }
+    __syncthreads();
+    const float Gi = Ghi[i], Gl = Glo[i];
+    Coef* cf = reinterpret_cast<Coef*>(img + kImgCoef);
+    const float eg = ex2_approx(Gi + Gl);
+    if (is_q) {
+      cf->oq[i] = eg * (rn * a.scale);
+    } else {
+      cf->eg[i] = eg * rn;
+      cf->ec[i] = i < n ? ex2_approx((Ghi[kC - 1] - Gi) + (Glo[kC - 1] - Gl)) * rn : 0.0f;
+      if (i == kC - 1) cf->decay = eg;
+    }
+    const int wi = 32 * (warp & 1);  // first token of this warp's rows
+    const float lead = is_q ? rn * a.scale : (i < n ? rn * beta[i] : 0.0f);
+    const int last = is_q ? i : i - 1;  // last column of this row
+#pragma unroll 1
+    for (int j = 0; j < wi + 32; j += 8) {
+      uint32_t d[8];
+      tmem_ld_x8(tmem + (static_cast<uint32_t>(32 * warp) << 16) + j, d);
+      tmem_ld_wait();
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const float4 gh = *reinterpret_cast<const float4*>(Ghi + j + e), gl = *reinterpret_cast<const float4*>(Glo + j + e);
+        const float4 rj = *reinterpret_cast<const float4*>(rk + j + e);
+        const float ghs[4] = {gh.x, gh.y, gh.z, gh.w}, gls[4] = {gl.x, gl.y, gl.z, gl.w};
+        const float rjs[4] = {rj.x, rj.y, rj.z, rj.w};
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          const float w = ex2_approx((Gi - ghs[z]) + (Gl - gls[z])) * rjs[z];
+          f[e + z] = j + e + z <= last ? lead * w * __uint_as_float(d[e + z]) : 0.0f;
+        }
+      }
+      if (is_q) {
+        if (j <= (i | 15)) {
+          uint32_t hi[4], mi[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) split2(pk2(f[2 * z], f[2 * z + 1]), hi[z], mi[z]);
+          unsigned char* p = img + kImgP + panel_piece(i, j >> 3);
+          *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(p + kPanelTerm) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+        }
+        __syncwarp();
+      } else {
+        float4* p = reinterpret_cast<float4*>(As + i * kALd + j);
+        p[0] = i < n ? make_float4(f[0], f[1], f[2], f[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        p[1] = i < n ? make_float4(f[4], f[5], f[6], f[7]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    __syncthreads();
+    const int col = lane;
+    if (!is_q) {
+      const float* Ab = As + wi * (kALd + 1);
+      float x[32];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        float acc[4] = {r == col ? 1.0f : 0.0f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < r; k += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(Ab + r * kALd + k);
+          acc[0] = fmaf(-w.x, x[k], acc[0]);
+          if (k + 1 < r) acc[1] = fmaf(-w.y, x[k + 1], acc[1]);
+          if (k + 2 < r) acc[2] = fmaf(-w.z, x[k + 2], acc[2]);
+          if (k + 3 < r) acc[3] = fmaf(-w.w, x[k + 3], acc[3]);
+        }
+        x[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < 32; ++r) As[(wi + r) * kALd + wi + col] = x[r];
+    }
+    __syncthreads();
+    {
+      // A21 T11 into the unused upper right block, then T21 over A21
+      float acc[8] = {};
+#pragma unroll 2
+      for (int k = 0; k < 32; k += 4) {
+        const float* w0 = As + k * kALd + col;
+        const float t0v = w0[0], t1v = w0[kALd], t2v = w0[2 * kALd], t3v = w0[3 * kALd];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float4 w = *reinterpret_cast<const float4*>(As + (32 + 8 * warp + r) * kALd + k);
+          acc[r] = fmaf(w.x, t0v, fmaf(w.y, t1v, fmaf(w.z, t2v, fmaf(w.w, t3v, acc[r]))));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) As[(8 * warp + r) * kALd + 32 + col] = acc[r], acc[r] = 0.0f;
+      __syncthreads();
+#pragma unroll 2
+      for (int k = 0; k < 32; k += 4) {
+        const float* w0 = As + k * kALd + 32 + col;
+        const float t0v = w0[0], t1v = w0[kALd], t2v = w0[2 * kALd], t3v = w0[3 * kALd];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float4 w = *reinterpret_cast<const float4*>(As + (32 + 8 * warp + r) * kALd + 32 + k);
+          acc[r] = fmaf(-w.x, t0v, fmaf(-w.y, t1v, fmaf(-w.z, t2v, fmaf(-w.w, t3v, acc[r]))));
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) As[(32 + 8 * warp + r) * kALd + col] = acc[r];
+    }
+    __syncthreads();
+    // T = the inverse times beta by column, three terms; thread: a row, every other 8 columns
+#pragma unroll 1
+    for (int j8 = pt >> 6; 8 * j8 <= (i | 15); j8 += 2) {
+      uint32_t hi[4], mi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const int j = 8 * j8 + e;
+        const float4 w = *reinterpret_cast<const float4*>(As + i * kALd + j);
+        const float4 b4 = *reinterpret_cast<const float4*>(beta + j);
+        split3(pk2(j <= i ? w.x * b4.x : 0.0f, j + 1 <= i ? w.y * b4.y : 0.0f), hi[e / 2], mi[e / 2], lo[e / 2]);
+        split3(pk2(j + 2 <= i ? w.z * b4.z : 0.0f, j + 3 <= i ? w.w * b4.w : 0.0f), hi[e / 2 + 1], mi[e / 2 + 1],
+               lo[e / 2 + 1]);
+      }
+      unsigned char* p = img + panel_piece(i, j8);
+      *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(p + kPanelTerm) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+      *reinterpret_cast<uint4*>(p + 2 * kPanelTerm) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    __syncthreads();
+  }
+  if (*abort && pt == 0) {  // a wait ran out: the loads and products end before the block does, with a limit
+    const uint64_t w0 = globaltimer_ns();
+    while (!mbar_try_wait(full, 0) && globaltimer_ns() - w0 < 2000000000ull) {
+    }
+    spin_ns(1000000);
+  }
+  __syncwarp();
+  if (warp == 0) {
+    tcgen05_fence_after();
+    tmem_dealloc(tmem, 64);
+  }
+}
+
+// ------------------------------------------------------------------- walk ---
+// One CTA per (sequence, head, 128 rows of d_value), 13 warps:
+//   warps 0-7   state: hold S (a thread: one row, half of the key channels),
+//               form the A operands between the products;
+//   warps 8-11  output: scale Q S^T where it lies, take the sum with the
+//               scores' product from there, round and store;
+//   warp 12     one thread issues the loads (two chunks in flight) and every MMA.
+constexpr int kStateWarps = 8, kCtlWarp = 12;
+constexpr int kChainThreads = 32 * 13;
+constexpr int kStages = 2;
+
+// Tensor memory, 512 columns.
+constexpr uint32_t kTmDelta = 0;  // the chunk's contribution to S; before it, R's three terms
+constexpr uint32_t kTmS = 128;    // S's three terms: half h at 96 h; then U's scaled terms in the second half
+constexpr uint32_t kTmY = 320;    // Y, then U
+constexpr uint32_t kTmO = 384;    // Q S^T, then with the scores' product
+constexpr uint32_t kTmU = 448;    // U's two output terms
+
+template <int KA>
+struct ChainSmem {
+  static constexpr int kKQ = KA * 2 * kAtom;  // per atom: K, then Q
+  static constexpr int kV = kKQ;              // [token][128]
+  static constexpr int kImg = kV + kC * 256;
+  static constexpr int kStage = (kImg + kImgStride + 1023) / 1024 * 1024;
+  static constexpr int kBad = kStages * kStage;  // int [2][128]
+  static constexpr int kBar = kBad + 2 * 128 * 4;
+  static constexpr int kMisc = kBar + (kStages + 14) * 8;  // TMEM address, abort flag
+  static constexpr int kTotal = kMisc + 16;
+  static_assert(kTotal + 1024 <= 232448, "227 KB of shared memory");
+  static constexpr uint32_t kTx = static_cast<uint32_t>(kImg + kImgBytes);
+};
+
+enum Bar {  // after the stages' full barriers; each completes once a chunk
+  kSReady0, kSReady1, kYDone, kOiDone, kRReady, kUDone, kUsReady, kSDone0, kSDone1, kUoReady, kOiRead, kOaDone, kOFree,
+  kNumNamed
+};
+static_assert(kNumNamed <= 14, "barrier count");
+
+template <int KA>
+__global__ void __launch_bounds__(kChainThreads, 1)
+    delta_chain_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, const unsigned char* img0,
+                       int slices) {
+  using M = ChainSmem<KA>;
   constexpr int DK = 64 * KA;
   constexpr int HC = DK / 2;   // key channels of a state thread
   constexpr int BLK = HC / 2;  // of one half-step of the state's conversion
@@ -202,31 +536,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int slice = static_cast<int>(blockIdx.x) % slices;
   const int unit = static_cast<int>(blockIdx.x) / slices;
   const int h = unit % static_cast<int>(a.H), s = unit / static_cast<int>(a.H);
-  const int grp = h / static_cast<int>(a.H / a.G);
-
-  int t0 = 0, len = static_cast<int>(a.L), seq = s;
-  if (a.cu) {
-    const int T = static_cast<int>(a.L);
-    t0 = min(max(a.cu[s], 0), T);
-    len = min(max(a.cu[s + 1], t0), T) - t0;
-    seq = 0;
-  }
-  const int nc = (len + kC - 1) / kC;
+  const Span sp = span_of(a, s);
+  const int nc = (sp.len + kC - 1) / kC;
 
   auto bar = [&](int b) { return sb + M::kBar + 8 * (kStages + b); };
-  auto full = [&](int st) { return sb + M::kBar + 8 * st; };
-  // 15 named barriers and one more: the output accumulator has been read.
-  const uint32_t o_free = sb + M::kMisc + 8;
+  auto full = [&](int c) { return sb + M::kBar + 8 * (c & 1); };
   volatile int* abort = reinterpret_cast<volatile int*>(smem + M::kMisc + 4);
   const Waiter wait{abort, a.err};
-  Coef* coefs = reinterpret_cast<Coef*>(smem + M::kCoef);
   int* bad = reinterpret_cast<int*>(smem + M::kBad);
 
   if (tid == 32 * kCtlWarp) {
-    for (int i = 0; i < kStages; ++i) mbar_init(full(i), 1);
-    const uint32_t counts[kNumNamed] = {1, 4, 4, 8, 8, 1, 1, 8, 1, 8, 1, 1, 8, 4, 1};
+    for (int i = 0; i < kStages; ++i) mbar_init(sb + M::kBar + 8 * i, 1);
+    const uint32_t counts[kNumNamed] = {8, 8, 1, 1, 8, 1, 8, 1, 1, 8, 4, 1, 4};
     for (int i = 0; i < kNumNamed; ++i) mbar_init(bar(i), counts[i]);
-    mbar_init(o_free, 4);
     *abort = 0;
     mbar_fence_init();
     prefetch_tensormap(&maps.q);
@@ -242,572 +564,340 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
-  const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;  // this warp's lane quarter
+  const uint32_t tm = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);  // this warp's lane quarter
+  const int row = 32 * (warp & 3) + lane;
+  const int64_t r = static_cast<int64_t>(slice) * 128 + row;
+  const bool row_in = r < a.dv;
+  auto arrive = [&](int b) {
+    tcgen05_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
 
   if (warp < kStateWarps) {
     // ------------------------------------------------------------- state ---
-    setmaxnreg_inc<kStateRegs>();
-    const int half = warp >> 2, row = 32 * (warp & 3) + lane;
-    const int64_t r = static_cast<int64_t>(slice) * 128 + row;
-    const bool row_in = r < a.dv;
+    const int half = warp >> 2;
     const int64_t sbase = ((static_cast<int64_t>(s) * a.H + h) * a.dv + (row_in ? r : 0)) * a.dk + half * HC;
     const int cols = static_cast<int>(min(static_cast<int64_t>(HC), max(a.dk - half * HC, static_cast<int64_t>(0))));
-    float S[HC];
+    uint64_t S[HC / 2];
 #pragma unroll
     for (int i = 0; i < HC; i += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (a.state_in && row_in && i < cols) v = *reinterpret_cast<const float4*>(a.state_in + sbase + i);
-      S[i] = v.x, S[i + 1] = v.y, S[i + 2] = v.z, S[i + 3] = v.w;
+      S[i / 2] = pk2(v.x, v.y), S[i / 2 + 1] = pk2(v.z, v.w);
     }
-    const uint32_t tm = tmem + lanes;
     float decay = 0.0f;
+    // 16 columns of S: decayed, with the last chunk's contribution
+    auto update = [&](int i0) {
+      uint32_t d[16];
+      tmem_ld_x16(tm + kTmDelta + half * HC + i0, d);
+      tmem_ld_wait();
+      const uint64_t dd = pk2(decay, decay);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) S[i0 / 2 + i] = ffma2(dd, S[i0 / 2 + i], pk2u(d[2 * i], d[2 * i + 1]));
+    };
+#pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
-      const Coef& cf = coefs[c & 3];
-      const int n = min(kC, len - kC * c);
-      // S, with the last chunk's contribution, as the A operand of Y and Q S^T
-      wait(bar(kTPReady), ph, 31);
+      unsigned char* stage = smem + ph * M::kStage;
+      const Coef& cf = *reinterpret_cast<const Coef*>(stage + M::kImg + kImgCoef);
+      const int n = min(kC, sp.len - kC * c);
+      // S as the A operand of Y and Q S^T
       if (c > 0) {
-        wait(bar(kSDone0 + half), ph ^ 1u, 32);
+        wait(bar(kSDone0 + half), ph ^ 1u, 33);
         tcgen05_fence_after();
+      }
+      if (a.cu && n < kC) {
+        // Keys behind the sequence (the next packed one's) meet zeros of U: they must be finite.
+        wait(full(c), (c >> 1) & 1, 34);
+        for (int e = tid; e < KA * kC * 8; e += 32 * kStateWarps) {
+          const int t = e / (kC * 8), i = e / 8 % kC;
+          if (i >= n) *reinterpret_cast<uint4*>(stage + t * 2 * kAtom + i * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
 #pragma unroll
         for (int i0 = b * BLK; i0 < (b + 1) * BLK; i0 += 16) {
-          float x[16];
-          if (c > 0) {
-            uint32_t d[16];
-            tmem_ld_x16(tm + kTmDelta + half * HC + i0, d);
-            tmem_ld_wait();
+          if (c > 0) update(i0);
+          uint64_t x[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[i0 + i] = fmaf(decay, S[i0 + i], __uint_as_float(d[i]));
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = S[i0 + i];
+          for (int i = 0; i < 8; ++i) x[i] = S[i0 / 2 + i];
           store_split3(tm + kTmS + half * 96 + i0 / 2, HC / 2, x);
         }
         tmem_st_wait();
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kSReady0 + b));
+        arrive(kSReady0 + b);
       }
-      decay = cf.decay;
       // R = V - e^G Y
-      const int st = c % kStages;
-      const unsigned char* vt = smem + st * M::kStage + M::kKQ + row * 2;
-      wait(full(st), (c / kStages) & 1, 33);
-      wait(bar(kYDone), ph, 34);
+      wait(full(c), (c >> 1) & 1, 34);
+      decay = cf.decay;
+      const unsigned char* vt = stage + M::kV + row * 2 + 32 * half * 256;
+      const float* eg = cf.eg + 32 * half;
+      wait(bar(kYDone), ph, 35);
       tcgen05_fence_after();
       uint32_t marks = 0;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int j0 = 32 * half + 16 * u;
+#pragma unroll 1
+      for (int u = 0; u < 32; u += 16) {
         uint32_t d[16];
-        float x[16];
-        tmem_ld_x16(tm + kTmY + j0, d);
+        uint64_t x[8];
+        tmem_ld_x16(tm + kTmY + 32 * half + u, d);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float v = __uint_as_float(static_cast<uint32_t>(
-                              *reinterpret_cast<const uint16_t*>(vt + (j0 + i) * 256)) << 16);
-          x[i] = j0 + i < n ? fmaf(-cf.eg[j0 + i], __uint_as_float(d[i]), v) : 0.0f;
+        for (int i = 0; i < 16; i += 4) {
+          const float4 e4 = *reinterpret_cast<const float4*>(eg + u + i);
+          float v[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            v[z] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vt + (u + i + z) * 256)) << 16);
+          x[i / 2] = ffma2(pk2(-e4.x, -e4.y), pk2u(d[i], d[i + 1]), pk2(v[0], v[1]));
+          x[i / 2 + 1] = ffma2(pk2(-e4.z, -e4.w), pk2u(d[i + 2], d[i + 3]), pk2(v[2], v[3]));
+        }
+        if (n < kC) {
+          const int left = n - 32 * half - u;  // tokens of the sequence from here
+          replace_marked(x, left >= 16 ? 0u : left <= 0 ? 0xffffu : 0xffffu << left & 0xffffu, 0.0f);
         }
         const uint32_t nf = not_finite(x);
-        if (nf) {
-          marks |= nf << (16 * u);
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (nf >> i & 1) x[i] = 0.0f;
-        }
-        __syncwarp();
-        store_split3(tm + kTmDelta + j0 / 2, 32, x);
+        replace_marked(x, nf, 0.0f);
+        marks |= nf << u;
+        store_split3(tm + kTmDelta + 16 * half + u / 2, 32, x);
       }
       tmem_st_wait();
-      tcgen05_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kRReady));
+      arrive(kRReady);
       // U: scaled into the state's product, plain into the output's
-      wait(bar(kUDone), ph, 35);
+      const float* ec = cf.ec + 32 * half;
+      wait(bar(kUDone), ph, 36);
       tcgen05_fence_after();
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int j0 = 32 * half + 16 * u;
+#pragma unroll 1
+      for (int u = 0; u < 32; u += 16) {
         uint32_t d[16];
-        float x[16];
-        tmem_ld_x16(tm + kTmY + j0, d);
+        uint64_t x[8];
+        tmem_ld_x16(tm + kTmY + 32 * half + u, d);
         tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(d[i]);
-        marks |= not_finite(x) << (16 * u);
+        for (int i = 0; i < 8; ++i) x[i] = pk2u(d[2 * i], d[2 * i + 1]);
+        marks |= not_finite(x) << u;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] *= cf.ec[j0 + i];
-        const uint32_t mk = marks >> (16 * u) & 0xffffu;
-        if (mk) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (mk >> i & 1) x[i] = __uint_as_float(0x7fffffffu);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 e4 = *reinterpret_cast<const float4*>(ec + u + i);
+          x[i / 2] = fmul2(x[i / 2], pk2(e4.x, e4.y));
+          x[i / 2 + 1] = fmul2(x[i / 2 + 1], pk2(e4.z, e4.w));
         }
-        __syncwarp();
-        store_split3(tm + kTmS + 96 + j0 / 2, 32, x);
+        replace_marked(x, marks >> u & 0xffffu, __uint_as_float(0x7fffffffu));
+        store_split3(tm + kTmS + 96 + 16 * half + u / 2, 32, x);
       }
       tmem_st_wait();
-      tcgen05_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kUsReady));
+      arrive(kUsReady);
       const int first = marks ? __ffs(marks) - 1 : 32;
       bad[half * 128 + row] = marks ? 32 * half + first : kC;
-      if (c + 1 < nc) wait(bar(kGFree), ph ^ 1u, 36);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
+#pragma unroll 1
+      for (int u = 0; u < 32; u += 16) {
         uint32_t d[16], hi[8], mi[8];
-        tmem_ld_x16(tm + kTmY + 32 * half + 16 * u, d);
+        uint64_t x[8];
+        tmem_ld_x16(tm + kTmY + 32 * half + u, d);
         tmem_ld_wait();
-        if (marks) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (16 * u + i >= first) d[i] = 0u;
-        }
-        __syncwarp();
+        for (int i = 0; i < 8; ++i) x[i] = pk2u(d[2 * i], d[2 * i + 1]);
+        replace_marked(x, first >= u + 16 ? 0u : first <= u ? 0xffffu : 0xffffu << (first - u) & 0xffffu, 0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          split2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]), hi[i], mi[i]);
-        tmem_st_x8(tm + kTmG + 16 * half + 8 * u, hi);
-        tmem_st_x8(tm + kTmG + 32 + 16 * half + 8 * u, mi);
+        for (int i = 0; i < 8; ++i) split2(x[i], hi[i], mi[i]);
+        tmem_st_x8(tm + kTmU + 16 * half + u / 2, hi);
+        tmem_st_x8(tm + kTmU + 32 + 16 * half + u / 2, mi);
       }
       tmem_st_wait();
-      tcgen05_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kUoReady));
+      arrive(kUoReady);
     }
     if (nc > 0) {
-      wait(bar(kSDone0 + half), (nc - 1) & 1, 32);
+      wait(bar(kSDone0 + half), (nc - 1) & 1, 33);
       tcgen05_fence_after();
 #pragma unroll
-      for (int i0 = 0; i0 < HC; i0 += 16) {
-        uint32_t d[16];
-        tmem_ld_x16(tm + kTmDelta + half * HC + i0, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) S[i0 + i] = fmaf(decay, S[i0 + i], __uint_as_float(d[i]));
-      }
+      for (int i0 = 0; i0 < HC; i0 += 16) update(i0);
     }
     if (row_in) {
 #pragma unroll
       for (int i = 0; i < HC; i += 4)
-        if (i < cols)
-          *reinterpret_cast<float4*>(a.state_out + sbase + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-    }
-  } else if (warp < kOutWarp) {
-    // -------------------------------------------------------------- prep ---
-    const int pt = tid - 32 * kPrepWarp;  // row of [K; Q]
-    const int i = pt & 63;                // its token
-    const bool is_q = pt >= 64;
-    float* As = reinterpret_cast<float*>(smem + M::kA);
-    float* Ghi = reinterpret_cast<float*>(smem + M::kVec);
-    float* Glo = Ghi + kC;
-    float* rk = Glo + kC;
-    float* betas = rk + kC;
-    const int64_t gb0 = static_cast<int64_t>(seq) * a.gb_seq + static_cast<int64_t>(t0) * a.gb_tok + h;
-    // g of tokens 2 l, 2 l + 1 in warp 0's lane l, beta of token pt - 64 in warps 2 and 3, one chunk ahead
-    auto fetch = [&](int c, float& x, float& y) {
-      x = y = 0.0f;
-      if (pt < 32) {
-        const int j = kC * c + 2 * pt;
-        if (j < len) x = a.g[gb0 + j * a.gb_tok];
-        if (j + 1 < len) y = a.g[gb0 + (j + 1) * a.gb_tok];
-      } else if (is_q) {
-        const int j = kC * c + i;
-        if (j < len) x = a.beta[gb0 + j * a.gb_tok];
-      }
-    };
-    float f0, f1;
-    fetch(0, f0, f1);
-    for (int c = 0; c < nc; ++c) {
-      const uint32_t ph = c & 1;
-      Coef& cf = coefs[c & 3];
-      float* beta = betas + ph * kC;
-      const int n = min(kC, len - kC * c);
-      const int st = c % kStages;
-      // Running sums of g in log2 units and fp64, kept as two floats: differences of far sums stay exact.
-      if (pt < 32) {
-        auto lg = [](float g) {
-          const double v = static_cast<double>(g) * 1.4426950408889634;
-          return v < -256.0 ? -256.0 : v;
-        };
-        const double g0 = lg(f0), g1 = lg(f1);
-        double sum = g0 + g1;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const double o = __shfl_up_sync(0xffffffffu, sum, d);
-          if (lane >= d) sum += o;
+        if (i < cols) {
+          float4 v;
+          upk2(S[i / 2], v.x, v.y);
+          upk2(S[i / 2 + 1], v.z, v.w);
+          *reinterpret_cast<float4*>(a.state_out + sbase + i) = v;
         }
-        const double first = sum - g1;
-        const float h0 = static_cast<float>(first), h1 = static_cast<float>(sum);
-        Ghi[2 * lane] = h0, Ghi[2 * lane + 1] = h1;
-        Glo[2 * lane] = static_cast<float>(first - h0), Glo[2 * lane + 1] = static_cast<float>(sum - h1);
-      } else if (is_q) {
-        beta[i] = f0;
-      }
-      if (c + 1 < nc) fetch(c + 1, f0, f1);
-      wait(full(st), (c / kStages) & 1, 37);
-      float rn = 1.0f;  // 1 / |row|
-      if (a.l2norm) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int t = 0; t < KA; ++t) {
-          const unsigned char* base = smem + st * M::kStage + t * 2 * M::kAtom + (is_q ? M::kAtom : 0);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint4 w = *reinterpret_cast<const uint4*>(base + sw128(i, j));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float lo = __uint_as_float(u[e] << 16), hi = __uint_as_float(u[e] & 0xffff0000u);
-              sum = fmaf(lo, lo, fmaf(hi, hi, sum));
-            }
-          }
-        }
-        rn = rsqrtf(sum + kL2Eps);
-      }
-      if (!is_q) rk[i] = rn;
-      named_bar_sync(kPrepBar, 128);
-      const float Gi = Ghi[i], Gl = Glo[i];
-      if (is_q) {
-        rn *= a.scale;
-        cf.oq[i] = ex2_approx(Gi + Gl) * rn;
-      } else {
-        cf.eg[i] = ex2_approx(Gi + Gl) * rn;
-        cf.ec[i] = i < n ? ex2_approx((Ghi[kC - 1] - Gi) + (Glo[kC - 1] - Gl)) * rn : 0.0f;
-        if (i == 0) cf.decay = ex2_approx(Ghi[kC - 1] + Glo[kC - 1]);
-      }
-      // This row of [K; Q] K^T
-      wait(bar(kGDone), ph, 38);
-      tcgen05_fence_after();
-      const int wi = 32 * ((warp >> 0) & 1);  // first token of this warp's rows
-      const float lead = is_q ? rn : rn * beta[i];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t d[32];
-        tmem_ld_x32(tmem + lanes + kTmG + 32 * b, d);
-        tmem_ld_wait();
-        if (b == 1) {
-          tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kGFree));
-        }
-        if (32 * b > wi) continue;  // columns behind every row of the warp: never read
-#pragma unroll
-        for (int j0 = 0; j0 < 32; j0 += 8) {
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const int j = 32 * b + j0 + e;
-            const float4 gh = *reinterpret_cast<const float4*>(Ghi + j), gl = *reinterpret_cast<const float4*>(Glo + j);
-            const float4 rj = *reinterpret_cast<const float4*>(rk + j);
-            const float ghs[4] = {gh.x, gh.y, gh.z, gh.w}, gls[4] = {gl.x, gl.y, gl.z, gl.w};
-            const float rjs[4] = {rj.x, rj.y, rj.z, rj.w};
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-              const float w = ex2_approx((Gi - ghs[z]) + (Gl - gls[z])) * rjs[z];
-              const bool keep = is_q ? j + z <= i : (j + z < i && i < n);
-              f[e + z] = keep ? lead * w * __uint_as_float(d[j0 + e + z]) : 0.0f;
-            }
-          }
-          const int j = 32 * b + j0;
-          if (is_q) {
-            uint32_t hi[4], mi[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) split2(f[2 * z], f[2 * z + 1], hi[z], mi[z]);
-            unsigned char* p = smem + M::kP + ph * 2 * M::kAtom + sw128(i, j >> 3);
-            *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(p + M::kAtom) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-          } else {
-            float4* p = reinterpret_cast<float4*>(As + i * kALd + j);
-            p[0] = make_float4(f[0], f[1], f[2], f[3]);
-            p[1] = make_float4(f[4], f[5], f[6], f[7]);
-          }
-        }
-      }
-      // Keys behind the sequence (the next packed sequence's) meet zeros of U: they must be finite.
-      if (a.cu && n < kC && !is_q && i >= n) {
-#pragma unroll
-        for (int t = 0; t < KA; ++t)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(smem + st * M::kStage + t * 2 * M::kAtom + sw128(i, j)) = make_uint4(0, 0, 0, 0);
-      }
-      named_bar_sync(kPrepBar, 128);
-      // (I + A)^-1: the two 32 x 32 diagonal blocks by substitution, a column per
-      // thread; then the block below them, -T22 (A21 T11), eight rows of a column
-      // per thread. The unused upper right block of As holds A21 T11.
-      const int col = lane, rg = warp & 3;
-      if (!is_q) {
-        const float* Ab = As + wi * (kALd + 1);
-        float x[32];
-#pragma unroll
-        for (int r = 0; r < 32; ++r) {
-          float acc[4] = {r == col ? 1.0f : 0.0f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < r; k += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(Ab + r * kALd + k);
-            acc[0] = fmaf(-w.x, x[k], acc[0]);
-            if (k + 1 < r) acc[1] = fmaf(-w.y, x[k + 1], acc[1]);
-            if (k + 2 < r) acc[2] = fmaf(-w.z, x[k + 2], acc[2]);
-            if (k + 3 < r) acc[3] = fmaf(-w.w, x[k + 3], acc[3]);
-          }
-          x[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int r = 0; r < 32; ++r) As[(wi + r) * kALd + wi + col] = x[r];
-      }
-      named_bar_sync(kPrepBar, 128);
-      {
-        float acc[8] = {};
-#pragma unroll 4
-        for (int k = 0; k < 32; k += 4) {
-          const float t0v = As[k * kALd + col], t1v = As[(k + 1) * kALd + col], t2v = As[(k + 2) * kALd + col],
-                      t3v = As[(k + 3) * kALd + col];
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const float4 w = *reinterpret_cast<const float4*>(As + (32 + 8 * rg + r) * kALd + k);
-            acc[r] = fmaf(w.x, t0v, fmaf(w.y, t1v, fmaf(w.z, t2v, fmaf(w.w, t3v, acc[r]))));
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) As[(8 * rg + r) * kALd + 32 + col] = acc[r];
-        named_bar_sync(kPrepBar, 128);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) acc[r] = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < 32; k += 4) {
-          const float* w0 = As + k * kALd + 32 + col;
-          const float t0v = w0[0], t1v = w0[kALd], t2v = w0[2 * kALd], t3v = w0[3 * kALd];
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const float4 w = *reinterpret_cast<const float4*>(As + (32 + 8 * rg + r) * kALd + 32 + k);
-            acc[r] = fmaf(-w.x, t0v, fmaf(-w.y, t1v, fmaf(-w.z, t2v, fmaf(-w.w, t3v, acc[r]))));
-          }
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) As[(32 + 8 * rg + r) * kALd + col] = acc[r];
-      }
-      named_bar_sync(kPrepBar, 128);
-      // T = the inverse times beta by column, three terms, once the last chunk's product has read the buffer
-      if (c > 0) wait(bar(kUDone), ph ^ 1u, 39);
-      {
-        const int r = pt >> 1, j0 = 32 * (pt & 1);
-#pragma unroll
-        for (int jj = 0; jj < 32; jj += 8) {
-          const int j = j0 + jj;
-          if (j > (r | 15)) continue;  // columns that no product reads
-          float f[8];
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            const float4 w = *reinterpret_cast<const float4*>(As + r * kALd + j + e);
-            const float4 b4 = *reinterpret_cast<const float4*>(beta + j + e);
-            f[e] = j + e <= r ? w.x * b4.x : 0.0f;
-            f[e + 1] = j + e + 1 <= r ? w.y * b4.y : 0.0f;
-            f[e + 2] = j + e + 2 <= r ? w.z * b4.z : 0.0f;
-            f[e + 3] = j + e + 3 <= r ? w.w * b4.w : 0.0f;
-          }
-          uint32_t hi[4], mi[4], lo[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) split3(f[2 * z], f[2 * z + 1], hi[z], mi[z], lo[z]);
-          unsigned char* p = smem + M::kT + sw128(r, j >> 3);
-          *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(p + M::kAtom) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-          *reinterpret_cast<uint4*>(p + 2 * M::kAtom) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kTPReady));
     }
   } else if (warp < kCtlWarp) {
     // ------------------------------------------------------------ output ---
-    setmaxnreg_dec<kOutRegs>();
-    const int row = 32 * (warp & 3) + lane;
-    const int64_t r = static_cast<int64_t>(slice) * 128 + row;
-    const bool row_in = r < a.dv;
-    __nv_bfloat16* op = a.out + static_cast<int64_t>(seq) * a.o_seq + static_cast<int64_t>(t0) * a.o_tok + h * a.dv +
-                        (row_in ? r : 0);
-    const uint32_t tm = tmem + lanes + kTmO;
+    __nv_bfloat16* op = a.out + static_cast<int64_t>(sp.seq) * a.o_seq + static_cast<int64_t>(sp.t0) * a.o_tok +
+                        h * a.dv + (row_in ? r : 0);
+#pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
-      const Coef& cf = coefs[c & 3];
-      const int n = min(kC, len - kC * c);
-      uint32_t d0[32], d1[32];
-      wait(bar(kOiDone), ph, 40);
+      const Coef& cf = *reinterpret_cast<const Coef*>(smem + ph * M::kStage + M::kImg + kImgCoef);
+      const int n = min(kC, sp.len - kC * c);
+      wait(full(c), (c >> 1) & 1, 37);
+      wait(bar(kOiDone), ph, 38);
       tcgen05_fence_after();
-      tmem_ld_x32(tm, d0);
-      tmem_ld_x32(tm + 32, d1);
-      tmem_ld_wait();
-      tcgen05_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kOiRead));
+#pragma unroll 1
+      for (int u = 0; u < kC; u += 16) {
+        uint32_t d[16];
+        tmem_ld_x16(tm + kTmO + u, d);
+        tmem_ld_wait();
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        d0[i] = __float_as_uint(cf.oq[i] * __uint_as_float(d0[i]));
-        d1[i] = __float_as_uint(cf.oq[32 + i] * __uint_as_float(d1[i]));
+        for (int i = 0; i < 16; i += 4) {
+          const float4 q4 = *reinterpret_cast<const float4*>(cf.oq + u + i);
+          const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) d[i + z] = __float_as_uint(__uint_as_float(d[i + z]) * qs[z]);
+        }
+        tmem_st_x16(tm + kTmO + u, d);
       }
-      wait(bar(kOaDone), ph, 41);
+      tmem_st_wait();
+      arrive(kOiRead);
+      wait(bar(kOaDone), ph, 39);
       tcgen05_fence_after();
       const int first = min(bad[row], bad[128 + row]);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        uint32_t e[16];
-        tmem_ld_x16(tm + 16 * b, e);
+#pragma unroll 1
+      for (int u = 0; u < kC; u += 16) {
+        uint32_t d[16];
+        tmem_ld_x16(tm + kTmO + u, d);
         tmem_ld_wait();
-        if (b == 3) {
-          tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_free);
-        }
+        if (u == kC - 16) arrive(kOFree);
+        if (first < u + 16) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = 16 * b + i;
-          const float inter = __uint_as_float(b < 2 ? d0[t & 31] : d1[t & 31]);
-          const float o = t < first ? inter + __uint_as_float(e[i]) : __uint_as_float(0x7fffffffu);
-          if (t < n && row_in) op[t * a.o_tok] = __float2bfloat16_rn(o);
+          for (int i = 0; i < 16; ++i)
+            if (u + i >= first) d[i] = 0x7fffffffu;
         }
+        if (row_in) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (u + i < n) *op = __float2bfloat16_rn(__uint_as_float(d[i]));
+            op += a.o_tok;
+          }
+        }
+        __syncwarp();
       }
-      op += kC * a.o_tok;
     }
-  } else {
+  } else if (lane == 0) {
     // ----------------------------------------------------------- control ---
-    setmaxnreg_dec<kCtlRegs>();
-    if (tid == 32 * kCtlWarp) {
+    const int grp = h / static_cast<int>(a.H / a.G);
+    const unsigned char* img = img0 + (slot_of(a, s, sp.t0) * a.H + h) * kImgStride;
+    int loaded = 0;
     auto load = [&](int c) {
       if (*abort) return;
-      const int st = c % kStages, tok = t0 + kC * c;
-      const uint32_t base = sb + st * M::kStage;
-      mbar_arrive_expect_tx(full(st), M::kTx);
+      const int tok = sp.t0 + kC * c;
+      const uint32_t base = sb + (c & 1) * M::kStage;
+      mbar_arrive_expect_tx(full(c), M::kTx);
 #pragma unroll
       for (int t = 0; t < KA; ++t) {
-        tma_load_4d(base + t * 2 * M::kAtom, &maps.k, 64 * t, grp, tok, seq, full(st));
-        tma_load_4d(base + t * 2 * M::kAtom + M::kAtom, &maps.q, 64 * t, grp, tok, seq, full(st));
+        tma_load_4d(base + t * 2 * kAtom, &maps.k, 64 * t, grp, tok, sp.seq, full(c));
+        tma_load_4d(base + t * 2 * kAtom + kAtom, &maps.q, 64 * t, grp, tok, sp.seq, full(c));
       }
-      tma_load_4d(base + M::kKQ, &maps.v, 128 * slice, h, tok, seq, full(st));
+      tma_load_4d(base + M::kV, &maps.v, 128 * slice, h, tok, sp.seq, full(c));
+      bulk_load(base + M::kImg, img + static_cast<int64_t>(c) * a.H * kImgStride, kImgBytes, full(c));
+      loaded = c + 1;
     };
-    int loaded = min(nc, kStages);
-    for (int c = 0; c < loaded; ++c) load(c);
-    auto katom = [&](int c, int t) { return sb + (c % kStages) * M::kStage + t * 2 * M::kAtom; };
-    auto scores = [&](int c) {  // [K; Q] K^T
-      wait(full(c % kStages), (c / kStages) & 1, 42);
-      tcgen05_fence_after();
-#pragma unroll
-      for (int t = 0; t < KA; ++t)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t d = umma_desc_k_sw128(katom(c, t) + 32 * kk);
-          umma_f16_ss(tmem + kTmG, d, d, chunk_idesc(64, false), t + kk > 0);
-        }
-      umma_commit(bar(kGDone));
-    };
-    if (nc > 0) scores(0);
-    if (nc > 1) {
-      wait(bar(kGFree), 0, 43);
-      tcgen05_fence_after();
-      scores(1);
-    }
+    for (int c = 0; c < min(nc, kStages); ++c) load(c);
+#pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
-      wait(bar(kTPReady), ph, 44);
+      const uint32_t stage = sb + ph * M::kStage;
+      const uint64_t kd = umma_desc_k_sw128(stage);
+      const uint64_t td = panel_desc(stage + M::kImg);
+      wait(full(c), (c >> 1) & 1, 40);
       // Y = S K^T, least terms first
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < 2; ++b) {
-        wait(bar(kSReady0 + b), ph, 45);
+        wait(bar(kSReady0 + b), ph, 41);
         tcgen05_fence_after();
-#pragma unroll
-        for (int t = 2; t >= 0; --t)
+#pragma unroll 1
+        for (int t = 2; t >= 0; --t) {
+          const uint32_t at = tmem + kTmS + t * (HC / 2) + b * BLK / 2;
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int ks = 0; ks < BLK / 16; ++ks) {
-              const int k = hf * HC + b * BLK + 16 * ks;
-              umma_f16_ts(tmem + kTmY, tmem + kTmS + hf * 96 + t * (HC / 2) + (b * BLK + 16 * ks) / 2,
-                          umma_desc_k_sw128(katom(c, k / 64) + (k % 64) * 2), chunk_idesc(64, false),
+              // key channels hf HC + b BLK + 16 ks ..: atom and byte within its rows
+              const int k0 = hf * HC + 16 * ks;
+              const uint32_t off = KA == 2 ? static_cast<uint32_t>(hf) * 2 * kAtom + (b * BLK + 16 * ks) * 2
+                                           : static_cast<uint32_t>(k0 + b * BLK) * 2;
+              umma_f16_ts(tmem + kTmY, at + hf * 96 + 8 * ks, desc_add(kd, off), chunk_idesc(64, false),
                           !(b == 0 && t == 2 && hf == 0 && ks == 0));
             }
+        }
       }
       umma_commit(bar(kYDone));
-      // every use of chunk c - 1's stage is over: its product into S has been read
-      if (c > 0 && c + kStages - 1 < nc) {
-        load(c + kStages - 1);
-        loaded = c + kStages;
+      // every use of the other stage is over: its chunk's last product is done
+      if (c > 0 && c + 1 < nc) {
+        wait(bar(kOaDone), ph ^ 1u, 47);
+        load(c + 1);
       }
       // Q S^T
-      if (c > 0) wait(o_free, ph ^ 1u, 46);
+      if (c > 0) wait(bar(kOFree), ph ^ 1u, 42);
       tcgen05_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int t = 1; t >= 0; --t)
 #pragma unroll
         for (int k = 0; k < DK; k += 16)
           umma_f16_ts(tmem + kTmO, tmem + kTmS + (k / HC) * 96 + t * (HC / 2) + (k % HC) / 2,
-                      umma_desc_k_sw128(katom(c, k / 64) + M::kAtom + (k % 64) * 2), chunk_idesc(64, false),
+                      desc_add(kd, (k / 64) * 2 * kAtom + kAtom + (k % 64) * 2), chunk_idesc(64, false),
                       !(t == 1 && k == 0));
       umma_commit(bar(kOiDone));
       // U = R T^T: 16 tokens j at a time meet the tokens i from theirs on
-      wait(bar(kRReady), ph, 47);
+      wait(bar(kRReady), ph, 43);
       tcgen05_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int pr = 0; pr < 6; ++pr) {
-        constexpr int kTt[6] = {2, 0, 1, 1, 0, 0}, kTr[6] = {0, 2, 1, 0, 1, 0};
+        const uint32_t tt = 0x201100u >> (4 * (5 - pr)) & 3u;  // terms of T and R, least products first
+        const uint32_t tr = 0x021010u >> (4 * (5 - pr)) & 3u;
+        const uint64_t d = desc_add(td, tt * kPanelTerm);
+        const uint32_t at = tmem + kTmDelta + 32 * tr;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(tmem + kTmY + 16 * kk, tmem + kTmDelta + 32 * kTr[pr] + 8 * kk,
-                      umma_desc_k_sw128(sb + M::kT + kTt[pr] * M::kAtom + 2048 * kk + 32 * kk),
-                      chunk_idesc(64 - 16 * kk, false), pr + kk > 0);
+          umma_f16_ts(tmem + kTmY + 16 * kk, at + 8 * kk, desc_add(d, panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
+                      pr + kk > 0);
       }
       umma_commit(bar(kUDone));
       // the chunk's contribution to S
-      wait(bar(kUsReady), ph, 48);
+      wait(bar(kUsReady), ph, 44);
       tcgen05_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int at = 0; at < KA; ++at) {
-#pragma unroll
+#pragma unroll 1
         for (int t = 2; t >= 0; --t)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             umma_f16_ts(tmem + kTmDelta + 64 * at, tmem + kTmS + 96 + 32 * t + 8 * kk,
-                        umma_desc_k_sw128(katom(c, at) + 2048 * kk), chunk_idesc(64, true), !(t == 2 && kk == 0));
+                        desc_add(kd, at * 2 * kAtom + 2048 * kk), chunk_idesc(64, true), !(t == 2 && kk == 0));
         umma_commit(bar(kSDone0 + at));
       }
       if (KA == 1) umma_commit(bar(kSDone1));
       // the scores times U
-      wait(bar(kOiRead), ph, 49);
-      wait(bar(kUoReady), ph, 50);
+      wait(bar(kOiRead), ph, 45);
+      wait(bar(kUoReady), ph, 46);
       tcgen05_fence_after();
-#pragma unroll
+#pragma unroll 1
       for (int pr = 0; pr < 3; ++pr) {
-        constexpr int kTp[3] = {1, 0, 0}, kTu[3] = {0, 1, 0};
+        const uint64_t d = desc_add(td, kImgP + (pr == 0 ? kPanelTerm : 0));
+        const uint32_t at = tmem + kTmU + (pr == 1 ? 32 : 0);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(tmem + kTmO + 16 * kk, tmem + kTmG + 32 * kTu[pr] + 8 * kk,
-                      umma_desc_k_sw128(sb + M::kP + (2 * ph + kTp[pr]) * M::kAtom + 2048 * kk + 32 * kk),
-                      chunk_idesc(64 - 16 * kk, false), pr + kk > 0);
+          umma_f16_ts(tmem + kTmO + 16 * kk, at + 8 * kk, desc_add(d, panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
+                      true);
       }
       umma_commit(bar(kOaDone));
-      if (c + 2 < nc) {
-        wait(bar(kOaDone), ph, 51);
-        scores(c + 2);
-      }
     }
     // Nothing is in flight at the end of a run whose waits all came: each load and product has been waited for.
     // Otherwise wait for them here, with a limit.
     if (*abort) {
-      for (int c = max(0, loaded - kStages); c < loaded; ++c)
-        for (uint64_t w0 = globaltimer_ns(); !mbar_try_wait(full(c % kStages), (c / kStages) & 1);)
-          if (globaltimer_ns() - w0 > 2000000000ull) break;
+      for (int c = max(0, loaded - kStages); c < loaded; ++c) {
+        const uint64_t w0 = globaltimer_ns();
+        while (!mbar_try_wait(full(c), (c >> 1) & 1) && globaltimer_ns() - w0 < 2000000000ull) {
+        }
+      }
       spin_ns(1000000);  // products take microseconds
     } else if (nc > 0) {
-      wait(bar(kOaDone), (nc - 1) & 1, 51);
+      wait(bar(kOaDone), (nc - 1) & 1, 39);
     }
-    }
-    __syncwarp();
   }
+  __syncwarp();
   tcgen05_fence_before();
   __syncthreads();
   if (warp == kCtlWarp) {
@@ -817,24 +907,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 }
 
 template <int KA>
-cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, cudaStream_t st) {
-  using M = ChunkSmem<KA>;
-  const int smem = M::kTotal + 1024;
-  auto kern = delta_chunk_kernel<KA>;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, int64_t slots, void* ws, cudaStream_t st) {
+  unsigned char* img = static_cast<unsigned char*>(ws);
+  const int prep_smem = PrepSmem<KA>::kTotal + 1024, smem = ChainSmem<KA>::kTotal + 1024;
+  auto prep = delta_prep_kernel<KA>;
+  auto chain = delta_chain_kernel<KA>;
+  cudaError_t err = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem);
+  if (err == cudaSuccess) err = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  cudaFuncAttributes attr;
-  const cudaError_t got = cudaFuncGetAttributes(&attr, kern);
-  if (got != cudaSuccess) return got;
-  if (attr.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;  // the register split would never complete
+  const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
+  prep<<<static_cast<unsigned>(slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
   const int slices = static_cast<int>((a.dv + 127) / 128);
-  kern<<<static_cast<unsigned>(a.batch * a.H * slices), kChunkThreads, smem, st>>>(maps, a, slices);
+  chain<<<static_cast<unsigned>(a.batch * a.H * slices), kChainThreads, smem, st>>>(maps, a, img, slices);
   return cudaGetLastError();
+}
+
+int64_t chunk_slots(int64_t batch, int64_t L, bool packed) {
+  return packed ? L / kC + batch : batch * ((L + kC - 1) / kC);
 }
 
 }  // namespace
 
-cudaError_t launch_delta_chunk(const DeltaArgs& a, cudaStream_t st) {
+size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, bool packed) {
+  return static_cast<size_t>(chunk_slots(batch, L, packed)) * static_cast<size_t>(H) * kImgStride;
+}
+
+cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st) {
   ChunkMaps m;
   const bool packed = a.cu != nullptr;
   auto map4 = [&](CUtensorMap* out, const void* base, int64_t n, int64_t heads, int64_t tok, int64_t seq,
@@ -848,7 +948,8 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a, cudaStream_t st) {
       !map4(&m.k, a.k, a.dk, a.G, a.k_tok, a.k_seq, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !map4(&m.v, a.v, a.dv, a.H, a.v_tok, a.v_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  return a.dk > 64 ? launch_chunk<2>(m, a, st) : launch_chunk<1>(m, a, st);
+  const int64_t slots = chunk_slots(a.batch, a.L, packed);
+  return a.dk > 64 ? launch_chunk<2>(m, a, slots, ws, st) : launch_chunk<1>(m, a, slots, ws, st);
 }
 
 }  // namespace ssm

@@ -75,6 +75,18 @@ def test_delta_rejects_bad_pointers(lib):
     assert delta_call(lib, d, cu=FAKE + 2) == _lib.SSM_ERR_INVALID_ARG
     assert delta_call(lib, delta_dims(seqlen=-1)) == _lib.SSM_ERR_INVALID_ARG
     assert delta_call(lib, delta_dims(seqlen=1 << 31)) == _lib.SSM_ERR_INVALID_ARG
+    need = lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(d), 0)
+    packed = lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(d), 1)
+    assert need == 2 * packed // 3 > 0  # two sequences of one chunk; 64 rows in two sequences: up to three chunks
+    assert need == api.delta_prefill_workspace_bytes(2, 64, 4, 2, 64, 128)
+    assert delta_call(lib, d, nbytes=need - 1) == _lib.SSM_ERR_INVALID_ARG
+    assert delta_call(lib, d, cu=FAKE, nbytes=packed - 1) == _lib.SSM_ERR_INVALID_ARG
+    assert delta_call(lib, d, work=None) == _lib.SSM_ERR_INVALID_ARG
+    assert delta_call(lib, d, work=FAKE + 16) == _lib.SSM_ERR_INVALID_ARG
+    assert lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(delta_dims(seqlen=1)), 0) == 0
+    assert lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(delta_dims(seqlen=0)), 1) == 0
+    assert lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(delta_dims(d_key=12)), 0) == 0
+    assert lib.ssm_delta_prefill_workspace_bytes(None, 0) == 0
     assert decode_call(lib, d, sin=None) == _lib.SSM_ERR_INVALID_ARG
     assert decode_call(lib, d, n=0) == _lib.SSM_ERR_INVALID_ARG
     assert decode_call(lib, d, n=1) == _lib.SSM_ERR_INVALID_ARG  # fewer states than rows, no index
