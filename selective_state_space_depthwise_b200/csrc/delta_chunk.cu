@@ -634,10 +634,15 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       decay = cf.decay;
       const unsigned char* vt = stage + M::kV + row * 2 + 32 * half * 256;
       const float* eg = cf.eg + 32 * half;
+      uint32_t v2[16];  // V, pairs of tokens, read while the product runs
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v2[i] = *reinterpret_cast<const uint16_t*>(vt + 2 * i * 256) |
+                static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vt + (2 * i + 1) * 256)) << 16;
       wait(bar(kYDone), ph, 35);
       tcgen05_fence_after();
       uint32_t marks = 0;
-#pragma unroll 1
+#pragma unroll
       for (int u = 0; u < 32; u += 16) {
         uint32_t d[16];
         uint64_t x[8];
@@ -646,12 +651,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 e4 = *reinterpret_cast<const float4*>(eg + u + i);
-          float v[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z)
-            v[z] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vt + (u + i + z) * 256)) << 16);
-          x[i / 2] = ffma2(pk2(-e4.x, -e4.y), pk2u(d[i], d[i + 1]), pk2(v[0], v[1]));
-          x[i / 2 + 1] = ffma2(pk2(-e4.z, -e4.w), pk2u(d[i + 2], d[i + 3]), pk2(v[2], v[3]));
+          const uint32_t va = v2[(u + i) / 2], vb = v2[(u + i) / 2 + 1];
+          x[i / 2] = ffma2(pk2(-e4.x, -e4.y), pk2u(d[i], d[i + 1]), pk2u(va << 16, va & 0xffff0000u));
+          x[i / 2 + 1] = ffma2(pk2(-e4.z, -e4.w), pk2u(d[i + 2], d[i + 3]), pk2u(vb << 16, vb & 0xffff0000u));
         }
         if (n < kC) {
           const int left = n - 32 * half - u;  // tokens of the sequence from here
@@ -775,24 +777,27 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         __syncwarp();
       }
     }
-  } else if (lane == 0) {
+  } else {
     // ----------------------------------------------------------- control ---
     const int grp = h / static_cast<int>(a.H / a.G);
     const unsigned char* img = img0 + (slot_of(a, s, sp.t0) * a.H + h) * kImgStride;
     int loaded = 0;
     auto load = [&](int c) {
       if (*abort) return;
-      const int tok = sp.t0 + kC * c;
-      const uint32_t base = sb + (c & 1) * M::kStage;
-      mbar_arrive_expect_tx(full(c), M::kTx);
-#pragma unroll
-      for (int t = 0; t < KA; ++t) {
-        tma_load_4d(base + t * 2 * kAtom, &maps.k, 64 * t, grp, tok, sp.seq, full(c));
-        tma_load_4d(base + t * 2 * kAtom + kAtom, &maps.q, 64 * t, grp, tok, sp.seq, full(c));
-      }
-      tma_load_4d(base + M::kV, &maps.v, 128 * slice, h, tok, sp.seq, full(c));
-      bulk_load(base + M::kImg, img + static_cast<int64_t>(c) * a.H * kImgStride, kImgBytes, full(c));
       loaded = c + 1;
+      if (elect_one()) {
+        const int tok = sp.t0 + kC * c;
+        const uint32_t base = sb + (c & 1) * M::kStage;
+        mbar_arrive_expect_tx(full(c), M::kTx);
+#pragma unroll
+        for (int t = 0; t < KA; ++t) {
+          tma_load_4d(base + t * 2 * kAtom, &maps.k, 64 * t, grp, tok, sp.seq, full(c));
+          tma_load_4d(base + t * 2 * kAtom + kAtom, &maps.q, 64 * t, grp, tok, sp.seq, full(c));
+        }
+        tma_load_4d(base + M::kV, &maps.v, 128 * slice, h, tok, sp.seq, full(c));
+        bulk_load(base + M::kImg, img + static_cast<int64_t>(c) * a.H * kImgStride, kImgBytes, full(c));
+      }
+      __syncwarp();
     };
     for (int c = 0; c < min(nc, kStages); ++c) load(c);
 #pragma unroll 1
@@ -803,27 +808,26 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const uint64_t td = panel_desc(stage + M::kImg);
       wait(full(c), (c >> 1) & 1, 40);
       // Y = S K^T, least terms first
-#pragma unroll 1
+#pragma unroll
       for (int b = 0; b < 2; ++b) {
         wait(bar(kSReady0 + b), ph, 41);
         tcgen05_fence_after();
-#pragma unroll 1
-        for (int t = 2; t >= 0; --t) {
-          const uint32_t at = tmem + kTmS + t * (HC / 2) + b * BLK / 2;
+        if (elect_one()) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
+          for (int t = 2; t >= 0; --t)
 #pragma unroll
-            for (int ks = 0; ks < BLK / 16; ++ks) {
-              // key channels hf HC + b BLK + 16 ks ..: atom and byte within its rows
-              const int k0 = hf * HC + 16 * ks;
-              const uint32_t off = KA == 2 ? static_cast<uint32_t>(hf) * 2 * kAtom + (b * BLK + 16 * ks) * 2
-                                           : static_cast<uint32_t>(k0 + b * BLK) * 2;
-              umma_f16_ts(tmem + kTmY, at + hf * 96 + 8 * ks, desc_add(kd, off), chunk_idesc(64, false),
-                          !(b == 0 && t == 2 && hf == 0 && ks == 0));
-            }
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int ks = 0; ks < BLK / 16; ++ks) {
+                const int k = hf * HC + b * BLK + 16 * ks;  // key channels k .. k + 15
+                umma_f16_ts(tmem + kTmY, tmem + kTmS + hf * 96 + t * (HC / 2) + (b * BLK + 16 * ks) / 2,
+                            desc_add(kd, (k / 64) * 2 * kAtom + (k % 64) * 2), chunk_idesc(64, false),
+                            !(b == 0 && t == 2 && hf == 0 && ks == 0));
+              }
+          if (b == 1) umma_commit(bar(kYDone));
         }
+        __syncwarp();
       }
-      umma_commit(bar(kYDone));
       // every use of the other stage is over: its chunk's last product is done
       if (c > 0 && c + 1 < nc) {
         wait(bar(kOaDone), ph ^ 1u, 47);
@@ -832,57 +836,65 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       // Q S^T
       if (c > 0) wait(bar(kOFree), ph ^ 1u, 42);
       tcgen05_fence_after();
-#pragma unroll 1
-      for (int t = 1; t >= 0; --t)
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < DK; k += 16)
-          umma_f16_ts(tmem + kTmO, tmem + kTmS + (k / HC) * 96 + t * (HC / 2) + (k % HC) / 2,
-                      desc_add(kd, (k / 64) * 2 * kAtom + kAtom + (k % 64) * 2), chunk_idesc(64, false),
-                      !(t == 1 && k == 0));
-      umma_commit(bar(kOiDone));
+        for (int t = 1; t >= 0; --t)
+#pragma unroll
+          for (int k = 0; k < DK; k += 16)
+            umma_f16_ts(tmem + kTmO, tmem + kTmS + (k / HC) * 96 + t * (HC / 2) + (k % HC) / 2,
+                        desc_add(kd, (k / 64) * 2 * kAtom + kAtom + (k % 64) * 2), chunk_idesc(64, false),
+                        !(t == 1 && k == 0));
+        umma_commit(bar(kOiDone));
+      }
+      __syncwarp();
       // U = R T^T: 16 tokens j at a time meet the tokens i from theirs on
       wait(bar(kRReady), ph, 43);
       tcgen05_fence_after();
-#pragma unroll 1
-      for (int pr = 0; pr < 6; ++pr) {
-        const uint32_t tt = 0x201100u >> (4 * (5 - pr)) & 3u;  // terms of T and R, least products first
-        const uint32_t tr = 0x021010u >> (4 * (5 - pr)) & 3u;
-        const uint64_t d = desc_add(td, tt * kPanelTerm);
-        const uint32_t at = tmem + kTmDelta + 32 * tr;
+      if (elect_one()) {
+        constexpr int kTt[6] = {2, 0, 1, 1, 0, 0}, kTr[6] = {0, 2, 1, 0, 1, 0};  // terms of T and R, least first
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(tmem + kTmY + 16 * kk, at + 8 * kk, desc_add(d, panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
-                      pr + kk > 0);
+        for (int pr = 0; pr < 6; ++pr)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_ts(tmem + kTmY + 16 * kk, tmem + kTmDelta + 32 * kTr[pr] + 8 * kk,
+                        desc_add(td, kTt[pr] * kPanelTerm + panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
+                        pr + kk > 0);
+        umma_commit(bar(kUDone));
       }
-      umma_commit(bar(kUDone));
+      __syncwarp();
       // the chunk's contribution to S
       wait(bar(kUsReady), ph, 44);
       tcgen05_fence_after();
-#pragma unroll 1
-      for (int at = 0; at < KA; ++at) {
-#pragma unroll 1
-        for (int t = 2; t >= 0; --t)
+      if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ts(tmem + kTmDelta + 64 * at, tmem + kTmS + 96 + 32 * t + 8 * kk,
-                        desc_add(kd, at * 2 * kAtom + 2048 * kk), chunk_idesc(64, true), !(t == 2 && kk == 0));
-        umma_commit(bar(kSDone0 + at));
+        for (int at = 0; at < KA; ++at) {
+#pragma unroll
+          for (int t = 2; t >= 0; --t)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ts(tmem + kTmDelta + 64 * at, tmem + kTmS + 96 + 32 * t + 8 * kk,
+                          desc_add(kd, at * 2 * kAtom + 2048 * kk), chunk_idesc(64, true), !(t == 2 && kk == 0));
+          umma_commit(bar(kSDone0 + at));
+        }
+        if (KA == 1) umma_commit(bar(kSDone1));
       }
-      if (KA == 1) umma_commit(bar(kSDone1));
+      __syncwarp();
       // the scores times U
       wait(bar(kOiRead), ph, 45);
       wait(bar(kUoReady), ph, 46);
       tcgen05_fence_after();
-#pragma unroll 1
-      for (int pr = 0; pr < 3; ++pr) {
-        const uint64_t d = desc_add(td, kImgP + (pr == 0 ? kPanelTerm : 0));
-        const uint32_t at = tmem + kTmU + (pr == 1 ? 32 : 0);
+      if (elect_one()) {
+        constexpr int kTp[3] = {1, 0, 0}, kTu[3] = {0, 1, 0};
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_f16_ts(tmem + kTmO + 16 * kk, at + 8 * kk, desc_add(d, panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
-                      true);
+        for (int pr = 0; pr < 3; ++pr)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_f16_ts(tmem + kTmO + 16 * kk, tmem + kTmU + 32 * kTu[pr] + 8 * kk,
+                        desc_add(td, kImgP + kTp[pr] * kPanelTerm + panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
+                        true);
+        umma_commit(bar(kOaDone));
       }
-      umma_commit(bar(kOaDone));
+      __syncwarp();
     }
     // Nothing is in flight at the end of a run whose waits all came: each load and product has been waited for.
     // Otherwise wait for them here, with a limit.
