@@ -64,7 +64,7 @@ constexpr int kAtom = kC * 128;   // 64 rows of 64 bf16: one swizzled operand at
 constexpr int kPanelTerm = (64 + 48 + 32 + 16) * 32;  // 5120 bytes of one term
 __host__ __device__ constexpr int panel_off(int kk) { return 32 * (64 * kk - 8 * kk * (kk - 1)); }
 struct Coef {
-  float eg[kC];  // e^{G_j} / |k_j|: scales Y
+  float neg[kC]; // -e^{G_j} / |k_j|: scales Y
   float ec[kC];  // e^{G_C - G_j} / |k_j|, 0 behind the sequence: scales U into the state
   float oq[kC];  // scale e^{G_i} / |q_i|: scales Q S^T
   float decay;   // e^{G_C}
@@ -201,16 +201,23 @@ __device__ __forceinline__ void replace_marked(uint64_t (&x)[8], uint32_t marks,
 }
 
 struct ChunkMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, out;
 };
 
 // ------------------------------------------------------------------- prep ---
 // One CTA of 4 warps per chunk and up to kPrepHeads heads of one key group,
 // four to an SM. Thread pt owns row pt of the 128 x 64 product [K; Q] K^T (one
 // set of MMAs per CTA; tensor memory keeps it for all its heads): rows 0-63
-// give A, rows 64-127 the scores. The inverse of I + A: the two 32 x 32
-// diagonal blocks by substitution, a column per thread; then the block below
-// them, -T22 (A21 T11), eight rows of a column per thread.
+// give A, rows 64-127 the scores.
+//
+// Decays. Within a row's own 16 columns each e^{G_i - G_j} is an exponential;
+// before them it is e^{G_i - G_m} e^{G_m - G_j}, m the token before the row's
+// 16: two factors that the row and the column bring along, neither above 1
+// where g <= 0, so that a product underflows only where the decay does.
+//
+// The inverse of I + A: 16 x 16 diagonal blocks by substitution (a block per
+// warp, a column per lane), then twice the block below a pair of inverted
+// ones, T21 = -T22 (A21 T11), first for 16 and then for 32 rows.
 constexpr int kPrepHeads = 4;
 constexpr int kALd = 68;  // floats between rows of A (16-byte rows, conflict-free columns)
 
@@ -218,10 +225,62 @@ template <int KA>  // 64-column atoms of d_key
 struct PrepSmem {
   // from 0, per atom: K, then Q
   static constexpr int kA = KA * 2 * kAtom;
-  static constexpr int kVec = kA + kC * kALd * 4;  // Ghi, Glo, rk, beta [64]
-  static constexpr int kBar = kVec + 4 * kC * 4;
+  static constexpr int kVec = kA + kC * kALd * 4;     // per head: Ghi, Glo, beta [64]
+  static constexpr int kRk = kVec + kPrepHeads * 3 * kC * 4;  // 1 / |k| [64]
+  static constexpr int kCf = kRk + kC * 4;            // column factors [3][64]
+  static constexpr int kBar = kCf + 3 * kC * 4;
   static constexpr int kTotal = kBar + 32;  // full, done, TMEM address, abort flag
 };
+
+// A fp32 value as two tf32 ones: 11 bits, and the rest (13 bits, of which the product reads 11).
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// One warp: the 16 x 8 NT block D = L R, L 16 x K and R K x 8 NT in As (row
+// stride kALd), K a multiple of 8; two tf32 terms each, three products (the
+// dropped one is 2^-22). 16-row blocks are far below the 128 rows of a
+// tcgen05 product, and in fp32 FMAs their operands' loads take the SM's whole
+// shared-memory bandwidth (4096 chunks and heads: 69 us; so: 59 us).
+template <int K, int NT>
+__device__ __forceinline__ void block_product(const float* L, const float* R, int lane, float (&c)[NT][4]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[j][e] = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; k += 8) {
+    uint32_t ah[4], al[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split_tf32(L[(g + 8 * (e & 1)) * kALd + k + t + 4 * (e >> 1)], ah[e], al[e]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      uint32_t bh[2], bl[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) split_tf32(R[(k + t + 4 * e) * kALd + 8 * j + g], bh[e], bl[e]);
+      mma_tf32(c[j], al, bh);
+      mma_tf32(c[j], ah, bl);
+      mma_tf32(c[j], ah, bh);
+    }
+  }
+}
+// Stores it, times sign.
+template <int NT>
+__device__ __forceinline__ void block_store(float* D, int lane, const float (&c)[NT][4], float sign) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    *reinterpret_cast<float2*>(D + g * kALd + 8 * j + 2 * t) = make_float2(sign * c[j][0], sign * c[j][1]);
+    *reinterpret_cast<float2*>(D + (g + 8) * kALd + 8 * j + 2 * t) = make_float2(sign * c[j][2], sign * c[j][3]);
+  }
+}
 
 template <int KA>
 __global__ void __launch_bounds__(128, 4)
@@ -280,8 +339,8 @@ __global__ void __launch_bounds__(128, 4)
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + M::kBar + 16);
-  wait(full, 0, 31);
-  if (pt == 0) {
+  if (pt == 96) {
+    wait(full, 0, 31);
 #pragma unroll
     for (int t = 0; t < KA; ++t)
 #pragma unroll
@@ -296,10 +355,36 @@ __global__ void __launch_bounds__(128, 4)
   const int i = pt & 63;  // this row's token
   const bool is_q = pt >= 64;
   float* As = reinterpret_cast<float*>(smem + M::kA);
-  float* Ghi = reinterpret_cast<float*>(smem + M::kVec);
-  float* Glo = Ghi + kC;
-  float* rk = Glo + kC;
-  float* beta = rk + kC;
+  float* rk = reinterpret_cast<float*>(smem + M::kRk);
+  float* cfac = reinterpret_cast<float*>(smem + M::kCf);
+  const int h0 = grp * rep + set * kPrepHeads, nh = min(kPrepHeads, rep - set * kPrepHeads);
+  // Warp w: head h0 + w. Running sums of g in log2 units and fp64, kept as two
+  // floats, so that differences of far sums stay exact; a decay below 2^-256 is 0 anyway.
+  if (warp < nh) {
+    float* vec = reinterpret_cast<float*>(smem + M::kVec) + warp * 3 * kC;
+    const int64_t gb = static_cast<int64_t>(sp.seq) * a.gb_seq + (static_cast<int64_t>(tok) + 2 * lane) * a.gb_tok + h0 + warp;
+    const bool in0 = 2 * lane < n, in1 = 2 * lane + 1 < n;
+    const float r0 = in0 ? a.g[gb] : 0.0f, r1 = in1 ? a.g[gb + a.gb_tok] : 0.0f;
+    const float b0 = in0 ? a.beta[gb] : 0.0f, b1 = in1 ? a.beta[gb + a.gb_tok] : 0.0f;
+    auto lg = [](float g) {
+      const double v = static_cast<double>(g) * 1.4426950408889634;
+      return v < -256.0 ? -256.0 : v;
+    };
+    const double g0 = lg(r0), g1 = lg(r1);
+    double sum = g0 + g1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const double o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const double first = sum - g1;
+    const float f0 = static_cast<float>(first), f1 = static_cast<float>(sum);
+    *reinterpret_cast<float2*>(vec + 2 * lane) = make_float2(f0, f1);
+    *reinterpret_cast<float2*>(vec + kC + 2 * lane) =
+        make_float2(static_cast<float>(first - f0), static_cast<float>(sum - f1));
+    *reinterpret_cast<float2*>(vec + 2 * kC + 2 * lane) = make_float2(b0, b1);
+  }
+  wait(full, 0, 31);
   float rn = 1.0f;  // 1 / |row|
   if (a.l2norm) {
     float s0 = 0.0f, s1 = 0.0f;
@@ -322,51 +407,83 @@ __global__ void __launch_bounds__(128, 4)
   if (!is_q) rk[i] = rn;
   wait(done, 0, 32);
   tcgen05_fence_after();
+  __syncthreads();
 
-  const int h0 = grp * rep + set * kPrepHeads, h1 = min(h0 + kPrepHeads, (grp + 1) * rep);
-  const int64_t gb0 = static_cast<int64_t>(sp.seq) * a.gb_seq + static_cast<int64_t>(tok) * a.gb_tok;
+  const uint32_t tmw = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+  const int b0 = 2 * (warp & 1), bi = i >> 4;  // 16-row blocks: this warp's first, this row's
+  const bool upper = lane < 16;                // the row is in the warp's first block
 #pragma unroll 1
-  for (int h = h0; h < h1; ++h) {
-    unsigned char* img = img0 + (slot * a.H + h) * kImgStride;
-    // Running sums of g in log2 units and fp64, kept as two floats: differences of far sums stay exact.
-    if (warp == 0) {
-      auto lg = [&](int j) {
-        const double v = j < n ? static_cast<double>(a.g[gb0 + j * a.gb_tok + h]) * 1.4426950408889634 : 0.0;
-        return v < -256.0 ? -256.0 : v;
-      };
-      const double g0 = lg(2 * lane), g1 = lg(2 * lane + 1);
-      double sum = g0 + g1;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      const double first = sum - g1;
-      const float f0 = static_cast<float>(first), f1 = static_cast<float>(sum);
-      Ghi[2 * lane] = f0, Ghi[2 * lane + 1] = f1;
-      Glo[2 * lane] = static_cast<float>(first - f0), Glo[2 * lane + 1] = static_cast<float>(sum - f1);
-    } else if (is_q) {
-      beta[i] = i < n ? a.beta[gb0 + i * a.gb_tok + h] : 0.0f;
-    }
-    __syncthreads();
+  for (int hh = 0; hh < nh; ++hh) {
+    const float* Ghi = reinterpret_cast<float*>(smem + M::kVec) + hh * 3 * kC;
+    const float* Glo = Ghi + kC;
+    const float* beta = Glo + kC;
+    unsigned char* img = img0 + (slot * a.H + h0 + hh) * kImgStride;
     const float Gi = Ghi[i], Gl = Glo[i];
     Coef* cf = reinterpret_cast<Coef*>(img + kImgCoef);
     const float eg = ex2_approx(Gi + Gl);
     if (is_q) {
       cf->oq[i] = eg * (rn * a.scale);
     } else {
-      cf->eg[i] = eg * rn;
+      cf->neg[i] = -eg * rn;
       cf->ec[i] = i < n ? ex2_approx((Ghi[kC - 1] - Gi) + (Glo[kC - 1] - Gl)) * rn : 0.0f;
       if (i == kC - 1) cf->decay = eg;
     }
-    const int wi = 32 * (warp & 1);  // first token of this warp's rows
-    const float lead = is_q ? rn * a.scale : (i < n ? rn * beta[i] : 0.0f);
-    const int last = is_q ? i : i - 1;  // last column of this row
+    {  // column factors of block row b, columns j < 16 b
+      const int b = pt < 48 ? 3 : pt < 96 ? 2 : 1, j = pt < 48 ? pt : pt < 96 ? pt - 64 : pt - 96;
+      if (j >= 0 && j < 16 * b) {
+        const int m = 16 * b - 1;
+        cfac[(b - 1) * kC + j] = ex2_approx((Ghi[m] - Ghi[j]) + (Glo[m] - Glo[j])) * rk[j];
+      }
+    }
+    __syncthreads();
+    const float lead = is_q ? rn * a.scale : rn * beta[i];
+    const float rfac = bi > 0 ? lead * ex2_approx((Gi - Ghi[16 * bi - 1]) + (Gl - Glo[16 * bi - 1])) : 0.0f;
+    // 8 values of this row from column j on: to A, or to the scores
+    auto put = [&](int j, float (&f)[8], bool mine) {
+      if (n < kC && !is_q && i >= n) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+      }
+      if (mine) {
+        if (is_q) {
+          uint32_t hi[4], mi[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) split2(pk2(f[2 * z], f[2 * z + 1]), hi[z], mi[z]);
+          unsigned char* p = img + kImgP + panel_piece(i, j >> 3);
+          *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(p + kPanelTerm) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
+        } else {
+          float4* p = reinterpret_cast<float4*>(As + i * kALd + j);
+          p[0] = make_float4(f[0], f[1], f[2], f[3]);
+          p[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+      }
+      __syncwarp();
+    };
+    auto before = [&](int j, const uint32_t (&d)[8], bool mine) {  // columns before the row's block
+      const float4* cp = reinterpret_cast<const float4*>(cfac + (bi > 0 ? bi - 1 : 0) * kC + j);
+      const float4 c0 = cp[0], c1 = cp[1];
+      const float cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = rfac * cv[e] * __uint_as_float(d[e]);
+      put(j, f, mine);
+    };
 #pragma unroll 1
-    for (int j = 0; j < wi + 32; j += 8) {
+    for (int j = 0; j < 16 * b0; j += 8) {
       uint32_t d[8];
-      tmem_ld_x8(tmem + (static_cast<uint32_t>(32 * warp) << 16) + j, d);
+      tmem_ld_x8(tmw + j, d);
       tmem_ld_wait();
+      before(j, d, true);
+    }
+#pragma unroll 1
+    for (int jj = 0; jj < 16; jj += 8) {
+      uint32_t d[8], e2[8];
+      tmem_ld_x8(tmw + 16 * b0 + jj, d);
+      tmem_ld_x8(tmw + 16 * b0 + 16 + jj, e2);
+      tmem_ld_wait();
+      before(16 * b0 + jj, d, !upper);
+      const int j = 16 * bi + jj, last = is_q ? i : i - 1;
       float f[8];
 #pragma unroll
       for (int e = 0; e < 8; e += 4) {
@@ -377,32 +494,18 @@ __global__ void __launch_bounds__(128, 4)
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
           const float w = ex2_approx((Gi - ghs[z]) + (Gl - gls[z])) * rjs[z];
-          f[e + z] = j + e + z <= last ? lead * w * __uint_as_float(d[e + z]) : 0.0f;
+          f[e + z] = j + e + z <= last ? lead * w * __uint_as_float(upper ? d[e + z] : e2[e + z]) : 0.0f;
         }
       }
-      if (is_q) {
-        if (j <= (i | 15)) {
-          uint32_t hi[4], mi[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) split2(pk2(f[2 * z], f[2 * z + 1]), hi[z], mi[z]);
-          unsigned char* p = img + kImgP + panel_piece(i, j >> 3);
-          *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(p + kPanelTerm) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
-        }
-        __syncwarp();
-      } else {
-        float4* p = reinterpret_cast<float4*>(As + i * kALd + j);
-        p[0] = i < n ? make_float4(f[0], f[1], f[2], f[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        p[1] = i < n ? make_float4(f[4], f[5], f[6], f[7]) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      put(j, f, true);
     }
     __syncthreads();
-    const int col = lane;
-    if (!is_q) {
-      const float* Ab = As + wi * (kALd + 1);
-      float x[32];
+    {  // diagonal blocks: warp w's, a column per lane (twice)
+      const int o = 16 * warp, col = lane & 15;
+      const float* Ab = As + o * (kALd + 1);
+      float x[16];
 #pragma unroll
-      for (int r = 0; r < 32; ++r) {
+      for (int r = 0; r < 16; ++r) {
         float acc[4] = {r == col ? 1.0f : 0.0f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < r; k += 4) {
@@ -415,38 +518,34 @@ __global__ void __launch_bounds__(128, 4)
         x[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
       }
       __syncwarp();
+      if (lane < 16) {
 #pragma unroll
-      for (int r = 0; r < 32; ++r) As[(wi + r) * kALd + wi + col] = x[r];
+        for (int r = 0; r < 16; ++r) As[(o + r) * kALd + o + col] = x[r];
+      }
     }
     __syncthreads();
-    {
-      // A21 T11 into the unused upper right block, then T21 over A21
-      float acc[8] = {};
-#pragma unroll 2
-      for (int k = 0; k < 32; k += 4) {
-        const float* w0 = As + k * kALd + col;
-        const float t0v = w0[0], t1v = w0[kALd], t2v = w0[2 * kALd], t3v = w0[3 * kALd];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float4 w = *reinterpret_cast<const float4*>(As + (32 + 8 * warp + r) * kALd + k);
-          acc[r] = fmaf(w.x, t0v, fmaf(w.y, t1v, fmaf(w.z, t2v, fmaf(w.w, t3v, acc[r]))));
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 8; ++r) As[(8 * warp + r) * kALd + 32 + col] = acc[r], acc[r] = 0.0f;
+    {  // 16 -> 32: two pairs, two warps each; the unused block right of a pair's first holds A21 T11
+      const int o = 32 * (warp >> 1), c0 = 8 * (warp & 1);
+      float c[1][4];
+      block_product<16, 1>(As + (o + 16) * kALd + o, As + o * kALd + o + c0, lane, c);
+      block_store<1>(As + o * kALd + o + 16 + c0, lane, c, 1.0f);
+      named_bar_sync(1 + (warp >> 1), 64);
+      block_product<16, 1>(As + (o + 16) * kALd + o + 16, As + o * kALd + o + 16 + c0, lane, c);
+      block_store<1>(As + (o + 16) * kALd + o + c0, lane, c, -1.0f);
+      // that block is zero in T11 and T22, which the next products read
+      named_bar_sync(1 + (warp >> 1), 64);
+      const float zero[1][4] = {};
+      block_store<1>(As + o * kALd + o + 16 + c0, lane, zero, 1.0f);
+    }
+    __syncthreads();
+    {  // 32 -> 64: 16 x 16 of the block per warp
+      const int r0 = 16 * (warp >> 1), c0 = 16 * (warp & 1);
+      float c[2][4];
+      block_product<32, 2>(As + (32 + r0) * kALd, As + c0, lane, c);
+      block_store<2>(As + r0 * kALd + 32 + c0, lane, c, 1.0f);
       __syncthreads();
-#pragma unroll 2
-      for (int k = 0; k < 32; k += 4) {
-        const float* w0 = As + k * kALd + 32 + col;
-        const float t0v = w0[0], t1v = w0[kALd], t2v = w0[2 * kALd], t3v = w0[3 * kALd];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float4 w = *reinterpret_cast<const float4*>(As + (32 + 8 * warp + r) * kALd + 32 + k);
-          acc[r] = fmaf(-w.x, t0v, fmaf(-w.y, t1v, fmaf(-w.z, t2v, fmaf(-w.w, t3v, acc[r]))));
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 8; ++r) As[(32 + 8 * warp + r) * kALd + col] = acc[r];
+      block_product<32, 2>(As + (32 + r0) * kALd + 32, As + 32 + c0, lane, c);
+      block_store<2>(As + (32 + r0) * kALd + c0, lane, c, -1.0f);
     }
     __syncthreads();
     // T = the inverse times beta by column, three terms; thread: a row, every other 8 columns
@@ -483,14 +582,17 @@ __global__ void __launch_bounds__(128, 4)
 }
 
 // ------------------------------------------------------------------- walk ---
-// One CTA per (sequence, head, 128 rows of d_value), 13 warps:
-//   warps 0-7   state: hold S (a thread: one row, half of the key channels),
-//               form the A operands between the products;
-//   warps 8-11  output: scale Q S^T where it lies, take the sum with the
+// One CTA per (sequence, head, 128 rows of d_value), 21 warps:
+//   warps 0-15  state: hold S (a thread: one row, a quarter of the key
+//               channels), form the A operands between the products. Four of
+//               them on each quarter of the SM keep its integer pipe busy (a
+//               pair of values in three terms takes 14 of its cycles) over the
+//               latencies of tensor memory, which two do not;
+//   warps 16-19 output: scale Q S^T where it lies, take the sum with the
 //               scores' product from there, round and store;
-//   warp 12     one thread issues the loads (two chunks in flight) and every MMA.
-constexpr int kStateWarps = 8, kCtlWarp = 12;
-constexpr int kChainThreads = 32 * 13;
+//   warp 20     one thread issues the loads (two chunks in flight) and every MMA.
+constexpr int kStateWarps = 16, kOutWarp = 16, kCtlWarp = 20;
+constexpr int kChainThreads = 32 * 21;
 constexpr int kStages = 2;
 
 // Tensor memory, 512 columns.
@@ -506,8 +608,9 @@ struct ChainSmem {
   static constexpr int kV = kKQ;              // [token][128]
   static constexpr int kImg = kV + kC * 256;
   static constexpr int kStage = (kImg + kImgStride + 1023) / 1024 * 1024;
-  static constexpr int kBad = kStages * kStage;  // int [2][128]
-  static constexpr int kBar = kBad + 2 * 128 * 4;
+  static constexpr int kOut = kStages * kStage;  // [token][128] bf16
+  static constexpr int kBad = kOut + kC * 256;   // int [4][128]
+  static constexpr int kBar = kBad + 4 * 128 * 4;
   static constexpr int kMisc = kBar + (kStages + 14) * 8;  // TMEM address, abort flag
   static constexpr int kTotal = kMisc + 16;
   static_assert(kTotal + 1024 <= 232448, "227 KB of shared memory");
@@ -526,8 +629,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
                        int slices) {
   using M = ChainSmem<KA>;
   constexpr int DK = 64 * KA;
-  constexpr int HC = DK / 2;   // key channels of a state thread
-  constexpr int BLK = HC / 2;  // of one half-step of the state's conversion
+  constexpr int HC = DK / 2;  // key channels of a half: of two state warpgroups
+  constexpr int QC = DK / 4;  // key channels of a state thread: KA steps of 16
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(smem);
@@ -547,13 +650,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
   if (tid == 32 * kCtlWarp) {
     for (int i = 0; i < kStages; ++i) mbar_init(sb + M::kBar + 8 * i, 1);
-    const uint32_t counts[kNumNamed] = {8, 8, 1, 1, 8, 1, 8, 1, 1, 8, 4, 1, 4};
+    const uint32_t counts[kNumNamed] = {16, 16, 1, 1, 16, 1, 16, 1, 1, 16, 4, 1, 4};
     for (int i = 0; i < kNumNamed; ++i) mbar_init(bar(i), counts[i]);
     *abort = 0;
     mbar_fence_init();
     prefetch_tensormap(&maps.q);
     prefetch_tensormap(&maps.k);
     prefetch_tensormap(&maps.v);
+    prefetch_tensormap(&maps.out);
   }
   if (warp == kCtlWarp) {
     __syncwarp();
@@ -576,12 +680,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
   if (warp < kStateWarps) {
     // ------------------------------------------------------------- state ---
-    const int half = warp >> 2;
-    const int64_t sbase = ((static_cast<int64_t>(s) * a.H + h) * a.dv + (row_in ? r : 0)) * a.dk + half * HC;
-    const int cols = static_cast<int>(min(static_cast<int64_t>(HC), max(a.dk - half * HC, static_cast<int64_t>(0))));
-    uint64_t S[HC / 2];
+    const int quarter = warp >> 2, half = quarter >> 1;
+    const int64_t sbase = ((static_cast<int64_t>(s) * a.H + h) * a.dv + (row_in ? r : 0)) * a.dk + quarter * QC;
+    const int cols = static_cast<int>(min(static_cast<int64_t>(QC), max(a.dk - quarter * QC, static_cast<int64_t>(0))));
+    uint64_t S[QC / 2];
 #pragma unroll
-    for (int i = 0; i < HC; i += 4) {
+    for (int i = 0; i < QC; i += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (a.state_in && row_in && i < cols) v = *reinterpret_cast<const float4*>(a.state_in + sbase + i);
       S[i / 2] = pk2(v.x, v.y), S[i / 2 + 1] = pk2(v.z, v.w);
@@ -590,12 +694,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     // 16 columns of S: decayed, with the last chunk's contribution
     auto update = [&](int i0) {
       uint32_t d[16];
-      tmem_ld_x16(tm + kTmDelta + half * HC + i0, d);
+      tmem_ld_x16(tm + kTmDelta + quarter * QC + i0, d);
       tmem_ld_wait();
       const uint64_t dd = pk2(decay, decay);
 #pragma unroll
       for (int i = 0; i < 8; ++i) S[i0 / 2 + i] = ffma2(dd, S[i0 / 2 + i], pk2u(d[2 * i], d[2 * i + 1]));
     };
+    const uint32_t tm_s = tm + kTmS + half * 96 + (quarter & 1) * (QC / 2);  // its columns of S's terms
+    const uint32_t tm_y = tm + kTmY + 16 * quarter;                          // its 16 tokens
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
@@ -617,94 +723,80 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         fence_proxy_async_smem();
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < KA; ++b) {
+        if (c > 0) update(16 * b);
+        uint64_t x[8];
 #pragma unroll
-        for (int i0 = b * BLK; i0 < (b + 1) * BLK; i0 += 16) {
-          if (c > 0) update(i0);
-          uint64_t x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = S[i0 / 2 + i];
-          store_split3(tm + kTmS + half * 96 + i0 / 2, HC / 2, x);
-        }
+        for (int i = 0; i < 8; ++i) x[i] = S[8 * b + i];
+        store_split3(tm_s + 8 * b, HC / 2, x);
         tmem_st_wait();
         arrive(kSReady0 + b);
       }
       // R = V - e^G Y
       wait(full(c), (c >> 1) & 1, 34);
       decay = cf.decay;
-      const unsigned char* vt = stage + M::kV + row * 2 + 32 * half * 256;
-      const float* eg = cf.eg + 32 * half;
-      uint32_t v2[16];  // V, pairs of tokens, read while the product runs
+      const unsigned char* vt = stage + M::kV + row * 2 + 16 * quarter * 256;
+      uint32_t v2[8];  // V, pairs of tokens, read while the product runs
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         v2[i] = *reinterpret_cast<const uint16_t*>(vt + 2 * i * 256) |
                 static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vt + (2 * i + 1) * 256)) << 16;
       wait(bar(kYDone), ph, 35);
       tcgen05_fence_after();
-      uint32_t marks = 0;
-#pragma unroll
-      for (int u = 0; u < 32; u += 16) {
+      uint32_t marks;
+      {
         uint32_t d[16];
         uint64_t x[8];
-        tmem_ld_x16(tm + kTmY + 32 * half + u, d);
+        tmem_ld_x16(tm_y, d);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          const float4 e4 = *reinterpret_cast<const float4*>(eg + u + i);
-          const uint32_t va = v2[(u + i) / 2], vb = v2[(u + i) / 2 + 1];
-          x[i / 2] = ffma2(pk2(-e4.x, -e4.y), pk2u(d[i], d[i + 1]), pk2u(va << 16, va & 0xffff0000u));
-          x[i / 2 + 1] = ffma2(pk2(-e4.z, -e4.w), pk2u(d[i + 2], d[i + 3]), pk2u(vb << 16, vb & 0xffff0000u));
+          const float4 e4 = *reinterpret_cast<const float4*>(cf.neg + 16 * quarter + i);
+          const uint32_t va = v2[i / 2], vb = v2[i / 2 + 1];
+          x[i / 2] = ffma2(pk2(e4.x, e4.y), pk2u(d[i], d[i + 1]), pk2u(va << 16, va & 0xffff0000u));
+          x[i / 2 + 1] = ffma2(pk2(e4.z, e4.w), pk2u(d[i + 2], d[i + 3]), pk2u(vb << 16, vb & 0xffff0000u));
         }
         if (n < kC) {
-          const int left = n - 32 * half - u;  // tokens of the sequence from here
+          const int left = n - 16 * quarter;  // tokens of the sequence from here
           replace_marked(x, left >= 16 ? 0u : left <= 0 ? 0xffffu : 0xffffu << left & 0xffffu, 0.0f);
         }
-        const uint32_t nf = not_finite(x);
-        replace_marked(x, nf, 0.0f);
-        marks |= nf << u;
-        store_split3(tm + kTmDelta + 16 * half + u / 2, 32, x);
+        marks = not_finite(x);
+        replace_marked(x, marks, 0.0f);
+        store_split3(tm + kTmDelta + 8 * quarter, 32, x);
       }
       tmem_st_wait();
       arrive(kRReady);
       // U: scaled into the state's product, plain into the output's
-      const float* ec = cf.ec + 32 * half;
       wait(bar(kUDone), ph, 36);
       tcgen05_fence_after();
-#pragma unroll 1
-      for (int u = 0; u < 32; u += 16) {
+      uint64_t x[8], y[8];
+      {
         uint32_t d[16];
-        uint64_t x[8];
-        tmem_ld_x16(tm + kTmY + 32 * half + u, d);
+        tmem_ld_x16(tm_y, d);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = pk2u(d[2 * i], d[2 * i + 1]);
-        marks |= not_finite(x) << u;
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 e4 = *reinterpret_cast<const float4*>(ec + u + i);
-          x[i / 2] = fmul2(x[i / 2], pk2(e4.x, e4.y));
-          x[i / 2 + 1] = fmul2(x[i / 2 + 1], pk2(e4.z, e4.w));
-        }
-        replace_marked(x, marks >> u & 0xffffu, __uint_as_float(0x7fffffffu));
-        store_split3(tm + kTmS + 96 + 16 * half + u / 2, 32, x);
       }
+      marks |= not_finite(x);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 e4 = *reinterpret_cast<const float4*>(cf.ec + 16 * quarter + i);
+        y[i / 2] = fmul2(x[i / 2], pk2(e4.x, e4.y));
+        y[i / 2 + 1] = fmul2(x[i / 2 + 1], pk2(e4.z, e4.w));
+      }
+      replace_marked(y, marks, __uint_as_float(0x7fffffffu));
+      store_split3(tm + kTmS + 96 + 8 * quarter, 32, y);
       tmem_st_wait();
       arrive(kUsReady);
-      const int first = marks ? __ffs(marks) - 1 : 32;
-      bad[half * 128 + row] = marks ? 32 * half + first : kC;
-#pragma unroll 1
-      for (int u = 0; u < 32; u += 16) {
-        uint32_t d[16], hi[8], mi[8];
-        uint64_t x[8];
-        tmem_ld_x16(tm + kTmY + 32 * half + u, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = pk2u(d[2 * i], d[2 * i + 1]);
-        replace_marked(x, first >= u + 16 ? 0u : first <= u ? 0xffffu : 0xffffu << (first - u) & 0xffffu, 0.0f);
+      const int first = marks ? __ffs(marks) - 1 : 16;
+      bad[quarter * 128 + row] = marks ? 16 * quarter + first : kC;
+      replace_marked(x, 0xffffu << first & 0xffffu, 0.0f);
+      {
+        uint32_t hi[8], mi[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2(x[i], hi[i], mi[i]);
-        tmem_st_x8(tm + kTmU + 16 * half + u / 2, hi);
-        tmem_st_x8(tm + kTmU + 32 + 16 * half + u / 2, mi);
+        tmem_st_x8(tm + kTmU + 8 * quarter, hi);
+        tmem_st_x8(tm + kTmU + 32 + 8 * quarter, mi);
       }
       tmem_st_wait();
       arrive(kUoReady);
@@ -713,11 +805,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       wait(bar(kSDone0 + half), (nc - 1) & 1, 33);
       tcgen05_fence_after();
 #pragma unroll
-      for (int i0 = 0; i0 < HC; i0 += 16) update(i0);
+      for (int i0 = 0; i0 < QC; i0 += 16) update(i0);
     }
     if (row_in) {
 #pragma unroll
-      for (int i = 0; i < HC; i += 4)
+      for (int i = 0; i < QC; i += 4)
         if (i < cols) {
           float4 v;
           upk2(S[i / 2], v.x, v.y);
@@ -727,8 +819,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
   } else if (warp < kCtlWarp) {
     // ------------------------------------------------------------ output ---
-    __nv_bfloat16* op = a.out + static_cast<int64_t>(sp.seq) * a.o_seq + static_cast<int64_t>(sp.t0) * a.o_tok +
-                        h * a.dv + (row_in ? r : 0);
+    __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem + M::kOut) + row;
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       const uint32_t ph = c & 1;
@@ -755,7 +846,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       arrive(kOiRead);
       wait(bar(kOaDone), ph, 39);
       tcgen05_fence_after();
-      const int first = min(bad[row], bad[128 + row]);
+      const int first = min(min(bad[row], bad[128 + row]), min(bad[256 + row], bad[384 + row]));
+      if (c > 0) {  // the last chunk's tile has been read
+        if (warp == kOutWarp && lane == 0) bulk_wait_read<0>();
+        named_bar_sync(1, 128);
+      }
 #pragma unroll 1
       for (int u = 0; u < kC; u += 16) {
         uint32_t d[16];
@@ -767,16 +862,27 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           for (int i = 0; i < 16; ++i)
             if (u + i >= first) d[i] = 0x7fffffffu;
         }
-        if (row_in) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (u + i < n) *op = __float2bfloat16_rn(__uint_as_float(d[i]));
-            op += a.o_tok;
-          }
-        }
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) tile[(u + i) * 128] = __float2bfloat16_rn(__uint_as_float(d[i]));
       }
+      // One tile store writes the chunk; it leaves out channels past d_value and tokens past L. The last tokens of
+      // a packed sequence end inside the tile: rows are written one by one.
+      if (!a.cu || n == kC) {
+        fence_proxy_async_smem();
+        named_bar_sync(1, 128);
+        if (warp == kOutWarp && lane == 0) {
+          tma_store_4d(&maps.out, sb + M::kOut, 128 * slice, h, sp.t0 + kC * c, sp.seq);
+          bulk_commit();
+        }
+      } else if (row_in) {
+        __nv_bfloat16* op = a.out + (static_cast<int64_t>(sp.t0) + kC * c) * a.o_tok + h * a.dv + r;
+        for (int t = 0; t < n; ++t) op[t * a.o_tok] = tile[t * 128];
+      }
+      __syncwarp();
     }
+    if (warp == kOutWarp && lane == 0) bulk_wait_read<0>();  // the tile stays until the last store has read it
+    __syncwarp();
   } else {
     // ----------------------------------------------------------- control ---
     const int grp = h / static_cast<int>(a.H / a.G);
@@ -809,22 +915,20 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       wait(full(c), (c >> 1) & 1, 40);
       // Y = S K^T, least terms first
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < KA; ++b) {
         wait(bar(kSReady0 + b), ph, 41);
         tcgen05_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int t = 2; t >= 0; --t)
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-              for (int ks = 0; ks < BLK / 16; ++ks) {
-                const int k = hf * HC + b * BLK + 16 * ks;  // key channels k .. k + 15
-                umma_f16_ts(tmem + kTmY, tmem + kTmS + hf * 96 + t * (HC / 2) + (b * BLK + 16 * ks) / 2,
-                            desc_add(kd, (k / 64) * 2 * kAtom + (k % 64) * 2), chunk_idesc(64, false),
-                            !(b == 0 && t == 2 && hf == 0 && ks == 0));
-              }
-          if (b == 1) umma_commit(bar(kYDone));
+            for (int w = 0; w < 4; ++w) {
+              const int k = w * QC + 16 * b;  // key channels k .. k + 15
+              umma_f16_ts(tmem + kTmY, tmem + kTmS + (w >> 1) * 96 + t * (HC / 2) + (w & 1) * (QC / 2) + 8 * b,
+                          desc_add(kd, (k / 64) * 2 * kAtom + (k % 64) * 2), chunk_idesc(64, false),
+                          !(b == 0 && t == 2 && w == 0));
+            }
+          if (b == KA - 1) umma_commit(bar(kYDone));
         }
         __syncwarp();
       }
@@ -958,7 +1062,8 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st) {
   };
   if (!map4(&m.q, a.q, a.dk, a.G, a.q_tok, a.q_seq, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !map4(&m.k, a.k, a.dk, a.G, a.k_tok, a.k_seq, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map4(&m.v, a.v, a.dv, a.H, a.v_tok, a.v_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
+      !map4(&m.v, a.v, a.dv, a.H, a.v_tok, a.v_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !map4(&m.out, a.out, a.dv, a.H, a.o_tok, a.o_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const int64_t slots = chunk_slots(a.batch, a.L, packed);
   return a.dk > 64 ? launch_chunk<2>(m, a, slots, ws, st) : launch_chunk<1>(m, a, slots, ws, st);
