@@ -395,13 +395,34 @@ def ssd_chunk_scan(cb, x, dt, dA_cumsum, C, prev_states, D=None, *, out=None, st
     return out
 
 
-def _device_stream(device, stream):
-    """The stream of the call on `device`: the one given, or that device's current stream. The tensors' device must
-    be the current one, on which the kernel is launched."""
-    if device.index is not None and device.index != torch.cuda.current_device():
-        raise RuntimeError(f"tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}: "
-                           "make the call under torch.cuda.device(...)")
-    return _stream(stream)
+try:  # the current stream's handle without a Stream object (3 us of a small call)
+    from torch._C import _cuda_getCurrentRawStream as _current_raw_stream
+except ImportError:
+    def _current_raw_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _raw_stream(device, stream):
+    """Handle of the call's stream on device number `device`, which must be the current one: kernels are launched
+    there."""
+    if device != torch.cuda.current_device():
+        raise RuntimeError(f"tensors are on cuda:{device}, but the current device is "
+                           f"cuda:{torch.cuda.current_device()}: make the call under torch.cuda.device(...)")
+    return _current_raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(names, *tensors):
+    """Device number that the tensors (or None) share; the first must be a tensor. names: theirs, in one string."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != device or device < 0):
+            for name, t in zip(names.split(), tensors):
+                _need_cuda(name, t, tensors[0].device)
+    return device
 
 
 def _stride(name, t, i):
@@ -409,14 +430,15 @@ def _stride(name, t, i):
     expanded dimension has no stride that the call could express."""
     if t.shape[i] <= 1 or not t.numel():
         return 0
-    if t.stride(i) == 0:
+    s = t.stride(i)
+    if s == 0:
         raise ValueError(f"{name} is expanded along dimension {i}: make it contiguous")
-    return t.stride(i)
+    return s
 
 
 def _row_stride(name, t):
     """The one stride between the rows of t [rows, dim] or [b, L, dim]."""
-    if t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"the rows of {name} must be contiguous")
     if t.dim() == 2:
         return _stride(name, t, 0)
@@ -428,45 +450,51 @@ def _row_stride(name, t):
 
 def _dense_heads(name, t):
     """The last two dimensions (head, channel) dense."""
-    if t.numel() and ((t.shape[-1] > 1 and t.stride(-1) != 1) or (t.shape[-2] > 1 and t.stride(-2) != t.shape[-1])):
+    h, c = t.shape[-2:]
+    if ((c > 1 and t.stride(-1) != 1) or (h > 1 and t.stride(-2) != c)) and t.numel():
         raise ValueError(f"the head and channel dimensions of {name} must be contiguous")
 
 
-def _delta_dims(q, k, v, g, beta, scale, qk_l2norm, lead):
-    """Checks the token tensors of the delta rule ([*lead, heads, channels]; g, beta [*lead, heads]) and fills the
-    shape part of SsmDeltaDims."""
-    n = len(lead)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _need_cuda(name, t, q.device)
-        if t.dtype != torch.bfloat16:
-            raise ValueError(f"{name} must be bfloat16")
-        if t.dim() != n + 2 or t.shape[:n] != lead:
-            raise ValueError(f"{name} must have shape [{'b, L' if n == 2 else 'tokens'}, heads, channels]")
-        _dense_heads(name, t)
-    H, G = v.shape[-2], q.shape[-2]
-    if k.shape != q.shape or G == 0 or H % G:
-        raise ValueError("k must have q's shape, and v's heads must be a multiple of q's")
-    for name, t in (("g", g), ("beta", beta)):
-        _need_cuda(name, t, q.device)
-        if t.dtype != torch.float32 or t.shape != lead + (H,) or (t.numel() and H > 1 and t.stride(-1) != 1):
-            raise ValueError(f"{name} must be float32 with one value per token and head of v, heads contiguous")
-    if g.stride() != beta.stride():
-        raise ValueError("g and beta must share strides")
-    if scale is not None and not scale > 0:
+_NO_STRIDES = (0,) * 10
+
+
+def _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, batch, seqlen, tokens, sequences):
+    """Checks the token tensors of the delta rule ([..., heads, channels]; g, beta [..., heads]) and fills
+    SsmDeltaDims; tokens, sequences: the dimensions that hold them, or None."""
+    qs, vs, bf16 = q.shape, v.shape, torch.bfloat16
+    lead, G, H = qs[:-2], qs[-2], vs[-2]
+    if q.dtype is not bf16 or k.dtype is not bf16 or v.dtype is not bf16 or out.dtype is not bf16:
+        raise ValueError("q, k, v and out must be bfloat16")
+    if k.shape != qs or vs[:-2] != lead or G == 0 or H % G:
+        raise ValueError("k must have q's shape, v its tokens, and v's heads must be a multiple of q's")
+    if out.shape != vs:
+        raise ValueError("out must have v's shape")
+    if g.dtype is not torch.float32 or beta.dtype is not torch.float32 or g.shape != vs[:-1] or beta.shape != vs[:-1]:
+        raise ValueError("g and beta must be float32 with one value per token and head of v")
+    if scale is None:
+        scale = 0.0
+    elif not scale > 0:
         raise ValueError("scale must be positive")
-    d = _lib.SsmDeltaDims()
-    d.nheads, d.ngroups, d.d_key, d.d_value = H, G, q.shape[-1], v.shape[-1]
-    d.scale, d.qk_l2norm = scale or 0.0, int(bool(qk_l2norm))
-    return d
+    if q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous() and g.is_contiguous() \
+            and beta.is_contiguous():
+        strides = _NO_STRIDES
+    else:
+        if H > 1 and g.numel() and (g.stride(-1) != 1 or beta.stride(-1) != 1):
+            raise ValueError("the heads of g and beta must be contiguous")
+        strides = []
+        for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("g", g)):
+            if t is not g:
+                _dense_heads(name, t)
+            strides.append(0 if tokens is None else _stride(name, t, tokens))
+            strides.append(0 if sequences is None else _stride(name, t, sequences))
+        if [0 if d is None else _stride("beta", beta, d) for d in (tokens, sequences)] != strides[8:]:
+            raise ValueError("g and beta must share strides")
+    return _lib.SsmDeltaDims(batch, seqlen, H, G, qs[-1], vs[-1], scale, 1 if qk_l2norm else 0, *strides)
 
 
-def _delta_state(name, t, n, dims, device):
-    _need_cuda(name, t, device)
-    if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 4
-                          or t.shape[1:] != (dims.nheads, dims.d_value, dims.d_key)
-                          or (n is not None and t.shape[0] != n)):
-        raise ValueError(f"{name} must be a contiguous float32 [{'states' if n is None else n}, {dims.nheads}, "
-                         f"{dims.d_value}, {dims.d_key}] tensor")
+def _delta_state(name, t, n, H, dv, dk):
+    if t.dtype is not torch.float32 or t.shape != (n, H, dv, dk) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [{n}, {H}, {dv}, {dk}] tensor")
 
 
 def delta_prefill_workspace_bytes(batch, seqlen, nheads, ngroups, d_key, d_value, packed=False) -> int:
@@ -487,41 +515,37 @@ def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=Non
     [n, H, dv, dk] fp32 or None = zeros; scale None = dk ** -0.5; qk_l2norm
     normalises q and k inside. Returns (out, state_out)."""
     lib = _lib.load()
-    lead = q.shape[:-2]
-    if len(lead) != (1 if cu_seqlens is not None else 2):
-        raise ValueError("q must be [b, L, G, dk], or [tokens, G, dk] with cu_seqlens")
-    dev = q.device
-    d = _delta_dims(q, k, v, g, beta, scale, qk_l2norm, lead)
-    if cu_seqlens is not None:
-        _need_cuda("cu_seqlens", cu_seqlens, dev)
-        if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
+    packed = cu_seqlens is not None
+    if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
+        raise ValueError("q must be [b, L, G, dk] and v [b, L, H, dv], or [tokens, ...] with cu_seqlens")
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    dev = _one_device("q k v g beta out state_in state_out cu_seqlens workspace", q, k, v, g, beta, out, state_in,
+                      state_out, cu_seqlens, workspace)
+    if packed:
+        if cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() \
                 or cu_seqlens.numel() < 2:
             raise ValueError("cu_seqlens must be a contiguous int32 [sequences + 1] tensor")
-        d.batch, d.seqlen = cu_seqlens.numel() - 1, lead[0]
+        n = cu_seqlens.numel() - 1
+        d = _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, n, q.shape[0], 0, None)
     else:
-        d.batch, d.seqlen = lead
-    if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    _need_cuda("out", out, dev)
-    if out.shape != v.shape or out.dtype != torch.bfloat16:
-        raise ValueError("out must be bfloat16 with v's shape")
-    _dense_heads("out", out)
-    _delta_state("state_in", state_in, d.batch, d, dev)
+        n = q.shape[0]
+        d = _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, n, q.shape[1], 1, 0)
+    H, dv, dk = v.shape[-2], v.shape[-1], q.shape[-1]
+    if state_in is not None:
+        _delta_state("state_in", state_in, n, H, dv, dk)
     if state_out is None:
-        state_out = torch.empty((d.batch, d.nheads, d.d_value, d.d_key), dtype=torch.float32, device=dev)
-    _delta_state("state_out", state_out, d.batch, d, dev)
-    d.q_tok_stride, d.k_tok_stride, d.v_tok_stride = _stride("q", q, -3), _stride("k", k, -3), _stride("v", v, -3)
-    d.out_tok_stride, d.gb_tok_stride = _stride("out", out, -3), _stride("g", g, -2)
-    if cu_seqlens is None:
-        d.q_seq_stride, d.k_seq_stride, d.v_seq_stride = _stride("q", q, 0), _stride("k", k, 0), _stride("v", v, 0)
-        d.out_seq_stride, d.gb_seq_stride = _stride("out", out, 0), _stride("g", g, 0)
-    ws = int(lib.ssm_delta_prefill_workspace_bytes(ctypes.byref(d), int(cu_seqlens is not None)))
+        state_out = torch.empty((n, H, dv, dk), dtype=torch.float32, device=q.device)
+    else:
+        _delta_state("state_out", state_out, n, H, dv, dk)
+    ref = ctypes.byref(d)
+    ws = lib.ssm_delta_prefill_workspace_bytes(ref, 1 if packed else 0)
     if ws and (workspace is None or workspace.numel() * workspace.element_size() < ws):
-        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
-    _need_cuda("workspace", workspace, dev)
-    _lib.check(lib.ssm_delta_prefill(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                     _ptr(cu_seqlens), _ptr(state_in), _ptr(out), _ptr(state_out),
-                                     _ptr(workspace) if ws else None, ws, _device_stream(dev, stream)))
+        workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
+    st = lib.ssm_delta_prefill(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                               _address(cu_seqlens), _address(state_in), out.data_ptr(), state_out.data_ptr(),
+                               workspace.data_ptr() if ws else None, ws, _raw_stream(dev, stream))
+    _lib.check(st)
     return out, state_out
 
 
@@ -534,28 +558,27 @@ def delta_decode_step(q, k, v, g, beta, state, *, state_index=None, scale=None, 
     each row, negative = padding, whose output and state are left alone; no two
     rows may name the same state. Returns out [b, H, dv]."""
     lib = _lib.load()
-    dev = q.device
-    d = _delta_dims(q, k, v, g, beta, scale, qk_l2norm, q.shape[:1])
-    d.batch, d.seqlen = q.shape[0], 1
-    if state_index is not None:
-        _need_cuda("state_index", state_index, dev)
-        if state_index.dtype != torch.int32 or state_index.shape != (d.batch,) or not state_index.is_contiguous():
-            raise ValueError("state_index must be a contiguous int32 [b] tensor")
-    _delta_state("state", state, None if state_index is not None else d.batch, d, dev)
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [b, G, dk] and v [b, H, dv]")
+    if out is None:
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
     if state_out is None:
         state_out = state
-    _delta_state("state_out", state_out, state.shape[0], d, dev)
-    if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=dev)
-    _need_cuda("out", out, dev)
-    if out.shape != v.shape or out.dtype != torch.bfloat16:
-        raise ValueError("out must be bfloat16 with v's shape")
-    _dense_heads("out", out)
-    d.q_seq_stride, d.k_seq_stride, d.v_seq_stride = _stride("q", q, 0), _stride("k", k, 0), _stride("v", v, 0)
-    d.out_seq_stride, d.gb_seq_stride = _stride("out", out, 0), _stride("g", g, 0)
-    _lib.check(lib.ssm_delta_decode_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                         _ptr(state_index), state.shape[0], _ptr(state), _ptr(out), _ptr(state_out),
-                                         _device_stream(dev, stream)))
+    dev = _one_device("q k v g beta state out state_out state_index", q, k, v, g, beta, state, out, state_out,
+                      state_index)
+    b, n = q.shape[0], state.shape[0]
+    d = _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, b, 1, None, 0)
+    if state_index is None:
+        n = b
+    elif state_index.dtype is not torch.int32 or state_index.shape != (b,) or not state_index.is_contiguous():
+        raise ValueError("state_index must be a contiguous int32 [b] tensor")
+    _delta_state("state", state, n, v.shape[1], v.shape[2], q.shape[2])
+    if state_out is not state:
+        _delta_state("state_out", state_out, n, v.shape[1], v.shape[2], q.shape[2])
+    st = lib.ssm_delta_decode_step(ctypes.byref(d), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                                   beta.data_ptr(), _address(state_index), n, state.data_ptr(), out.data_ptr(),
+                                   state_out.data_ptr(), _raw_stream(dev, stream))
+    _lib.check(st)
     return out
 
 
@@ -568,31 +591,35 @@ def gated_norm(x, z, weight, *, group_size=None, eps=1e-5, gate_first=False, out
     fp32 [dim], or [group_size] for every group alike. out may be x or z.
     Returns out."""
     lib = _lib.load()
-    dev = x.device
-    if x.dim() not in (2, 3) or x.dtype not in _DTYPES:
+    shape = x.shape
+    n = len(shape)
+    if (n != 2 and n != 3) or x.dtype not in _DTYPES:
         raise ValueError("x must be a float32 or bfloat16 [rows, dim] or [b, L, dim] tensor")
-    dim = x.shape[-1]
+    dim = shape[-1]
     group = dim if group_size is None else int(group_size)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    for n, t in (("x", x), ("z", z), ("out", out)):
-        _need_cuda(n, t, dev)
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or (t.numel() and dim > 1 and t.stride(-1) != 1)):
-            raise ValueError(f"{n} must have x's shape and dtype and a contiguous last dimension")
-    _need_cuda("weight", weight, dev)
-    if weight.dtype != torch.float32 or not weight.is_contiguous() or weight.shape not in ((dim,), (group,)):
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    dev = _one_device("x z out weight", x, z, out, weight)
+    strides = []
+    for name, t in (("x", x), ("z", z), ("out", out)):
+        if t is None:
+            strides += (0, 0)
+            continue
+        if t.shape == shape and t.dtype is x.dtype and t.is_contiguous():
+            strides += (0, 0)
+            continue
+        if t.shape != shape or t.dtype is not x.dtype or (t.stride(-1) != 1 and dim > 1 and t.numel()):
+            raise ValueError(f"{name} must have x's shape and dtype and a contiguous last dimension")
+        strides.append(_stride(name, t, n - 2))
+        strides.append(_stride(name, t, 0) if n == 3 else 0)
+    ws = weight.shape
+    if weight.dtype is not torch.float32 or len(ws) != 1 or ws[0] not in (dim, group) or not weight.is_contiguous():
         raise ValueError("weight must be contiguous float32 [dim] or [group_size]")
-    d = _lib.SsmGatedNormDims()
-    d.batch, d.seqlen = (1, x.shape[0]) if x.dim() == 2 else x.shape[:2]
-    d.dim, d.group, d.eps, d.io_dtype = dim, group, eps, _DTYPES[x.dtype]
-    d.gate_first, d.shared_weight = int(bool(gate_first)), int(weight.shape[0] != dim)
-    d.x_tok_stride, d.y_tok_stride = _stride("x", x, -2), _stride("out", out, -2)
-    d.z_tok_stride = 0 if z is None else _stride("z", z, -2)
-    if x.dim() == 3:
-        d.x_seq_stride, d.y_seq_stride = _stride("x", x, 0), _stride("out", out, 0)
-        d.z_seq_stride = 0 if z is None else _stride("z", z, 0)
-    _lib.check(lib.ssm_gated_norm(ctypes.byref(d), _ptr(x), _ptr(z), _ptr(weight), _ptr(out),
-                                  _device_stream(dev, stream)))
+    d = _lib.SsmGatedNormDims(1 if n == 2 else shape[0], shape[n - 2], dim, group, eps, _DTYPES[x.dtype],
+                              1 if gate_first else 0, 0 if ws[0] == dim else 1, *strides)
+    st = lib.ssm_gated_norm(ctypes.byref(d), x.data_ptr(), _address(z), weight.data_ptr(), out.data_ptr(),
+                            _raw_stream(dev, stream))
+    _lib.check(st)
     return out
 
 
@@ -605,37 +632,40 @@ def residual_norm(x, residual, weight, *, post_weight=None, residual_scale=1.0, 
     first block; residual_dtype then picks r's type, default x's); weights fp32
     [dim]. residual_out may be residual. Returns (out, residual_out)."""
     lib = _lib.load()
-    dev = x.device
-    if x.dim() not in (2, 3) or x.dtype not in _DTYPES:
+    shape, dt = x.shape, x.dtype
+    if len(shape) not in (2, 3) or dt not in _DTYPES:
         raise ValueError("x must be a float32 or bfloat16 [rows, dim] or [b, L, dim] tensor")
-    dim = x.shape[-1]
-    rdt = residual.dtype if residual is not None else residual_dtype or (
-        residual_out.dtype if residual_out is not None else x.dtype)
+    dim = shape[-1]
+    if residual is not None:
+        rdt = residual.dtype
+    else:
+        rdt = residual_dtype or (residual_out.dtype if residual_out is not None else dt)
     if rdt not in _DTYPES or (residual_dtype is not None and residual_dtype != rdt):
         raise ValueError("the residual must be float32 or bfloat16, of residual_dtype where that is given")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty(shape, dtype=dt, device=x.device)
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=rdt, device=dev)
-    d = _lib.SsmResidualNormDims()
-    for n, t, dt in (("x", x, x.dtype), ("residual", residual, rdt), ("out", out, x.dtype),
-                     ("residual_out", residual_out, rdt)):
-        _need_cuda(n, t, dev)
+        residual_out = torch.empty(shape, dtype=rdt, device=x.device)
+    dev = _one_device("x residual out residual_out weight post_weight", x, residual, out, residual_out, weight,
+                      post_weight)
+    strides = []
+    for name, t, want in (("x", x, dt), ("residual", residual, rdt), ("out", out, dt),
+                          ("residual_out", residual_out, rdt)):
         if t is None:
+            strides.append(0)
             continue
-        if t.shape != x.shape or t.dtype != dt:
-            raise ValueError(f"{n} must be a {dt} tensor of x's shape")
-    for n, t in (("weight", weight), ("post_weight", post_weight)):
-        _need_cuda(n, t, dev)
-        if t is not None and (t.dtype != torch.float32 or t.shape != (dim,) or not t.is_contiguous()):
-            raise ValueError(f"{n} must be contiguous float32 [dim]")
-    d.rows, d.dim, d.eps, d.residual_scale = x.numel() // max(dim, 1), dim, eps, residual_scale
-    d.io_dtype, d.residual_dtype = _DTYPES[x.dtype], _DTYPES[rdt]
-    d.x_stride, d.y_stride, d.residual_out_stride = (_row_stride("x", x), _row_stride("out", out),
-                                                     _row_stride("residual_out", residual_out))
-    d.residual_in_stride = 0 if residual is None else _row_stride("residual", residual)
-    _lib.check(lib.ssm_residual_norm(ctypes.byref(d), _ptr(x), _ptr(residual), _ptr(weight), _ptr(post_weight),
-                                     _ptr(out), _ptr(residual_out), _device_stream(dev, stream)))
+        if t.shape != shape or t.dtype is not want:
+            raise ValueError(f"{name} must be a {want} tensor of x's shape")
+        strides.append(0 if t.is_contiguous() else _row_stride(name, t))
+    for name, t in (("weight", weight), ("post_weight", post_weight)):
+        if t is not None and (t.dtype is not torch.float32 or t.shape != (dim,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous float32 [dim]")
+    d = _lib.SsmResidualNormDims(x.numel() // max(dim, 1), dim, eps, residual_scale, _DTYPES[dt], _DTYPES[rdt],
+                                 *strides)
+    st = lib.ssm_residual_norm(ctypes.byref(d), x.data_ptr(), _address(residual), weight.data_ptr(),
+                               _address(post_weight), out.data_ptr(), residual_out.data_ptr(),
+                               _raw_stream(dev, stream))
+    _lib.check(st)
     return out, residual_out
 
 
@@ -698,7 +728,7 @@ def residual_block_forward(x, residual, params, proj, norm_weight, *, post_weigh
         ctypes.byref(dims), ctypes.byref(w), ctypes.byref(pw), ctypes.byref(nw), _ptr(x), _ptr(residual),
         _ptr(conv_cache_in), _ptr(ssm_state_in), _ptr(residual_out), _ptr(out), _ptr(conv_cache_out),
         _ptr(ssm_state_out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _device_stream(dev, stream)))
+        _raw_stream(x.get_device(), stream)))
     return out, residual_out, conv_cache_out, ssm_state_out
 
 

@@ -43,6 +43,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "delta_internal.h"
 #include "sm100_ptx.cuh"
 #include "ssm.h"
@@ -312,6 +314,7 @@ __global__ void __launch_bounds__(128, 4)
     s = static_cast<int>(slot / nc), c = static_cast<int>(slot % nc);
   }
   const Span sp = span_of(a, s);
+  griddep_launch_dependents();  // the walk may set up; it waits for this grid before it reads the workspace
   if (c < 0 || kC * c >= sp.len) return;
   const int n = min(kC, sp.len - kC * c), tok = sp.t0 + kC * c;
 
@@ -905,6 +908,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       __syncwarp();
     };
+    griddep_wait();  // the prep's workspace
     for (int c = 0; c < min(nc, kStages); ++c) load(c);
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
@@ -1028,16 +1032,33 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, int64_t slot
   const int prep_smem = PrepSmem<KA>::kTotal + 1024, smem = ChainSmem<KA>::kTotal + 1024;
   auto prep = delta_prep_kernel<KA>;
   auto chain = delta_chain_kernel<KA>;
-  cudaError_t err = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem);
-  if (err == cudaSuccess) err = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The kernels' shared-memory limits, once per device.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    err = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
   const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
   prep<<<static_cast<unsigned>(slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   const int slices = static_cast<int>((a.dv + 127) / 128);
-  chain<<<static_cast<unsigned>(a.batch * a.H * slices), kChainThreads, smem, st>>>(maps, a, img, slices);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch * a.H * slices));
+  cfg.blockDim = dim3(kChainThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chain, maps, a, static_cast<const unsigned char*>(img), slices);
 }
 
 int64_t chunk_slots(int64_t batch, int64_t L, bool packed) {
