@@ -626,10 +626,25 @@ enum Bar {  // after the stages' full barriers; each completes once a chunk
 };
 static_assert(kNumNamed <= 14, "barrier count");
 
-template <int KA>
+// A long sequence with few heads leaves most SMs idle, so it may be walked in
+// `count` segments of `per` chunks at once. The state is linear in the one
+// before it: S_{p+1} = S_p M_p + H_p, H_p a segment's walk from zero and M_p
+// its walk of the identity without values. Pass 1 (states only, OUT = false)
+// forms both for every segment that needs them, segment 0 from the state given;
+// delta_join_kernel folds them into the segments' first states; pass 2 walks
+// all segments. More than twice the work of one walk, on more than twice the SMs.
+struct Segments {
+  int count, per;  // count 1: one walk
+  float* S;        // [sequence, head][count][d_value][d_key]: the segments' first states
+  float* M;        // [sequence, head][count - 2][d_key][d_key]: M_1 ..
+};
+
+constexpr int kOrderSeqs = 256;  // packed sequences up to which the walk starts with the longest
+
+template <int KA, bool OUT>
 __global__ void __launch_bounds__(kChainThreads, 1)
     delta_chain_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, const unsigned char* img0,
-                       int slices) {
+                       int slices, const Segments sg) {
   using M = ChainSmem<KA>;
   constexpr int DK = 64 * KA;
   constexpr int HC = DK / 2;  // key channels of a half: of two state warpgroups
@@ -639,10 +654,43 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int slice = static_cast<int>(blockIdx.x) % slices;
-  const int unit = static_cast<int>(blockIdx.x) / slices;
-  const int h = unit % static_cast<int>(a.H), s = unit / static_cast<int>(a.H);
-  const Span sp = span_of(a, s);
+  // This block's sequence, head, rows and segment; `ident`: it walks the identity.
+  const int H = static_cast<int>(a.H);
+  int unit = static_cast<int>(blockIdx.x), seg = 0;
+  bool ident = false;
+  if constexpr (OUT) {
+    seg = unit % sg.count, unit /= sg.count;
+  } else {
+    const int walks = static_cast<int>(a.batch) * H * slices * (sg.count - 1);
+    ident = unit >= walks;
+    if (ident) {
+      unit -= walks;
+      seg = 1 + unit % (sg.count - 2), unit = unit / (sg.count - 2) * slices;
+    } else {
+      seg = unit % (sg.count - 1), unit /= sg.count - 1;
+    }
+  }
+  const int slice = unit % slices, sh = unit / slices, h = sh % H;
+  int s = sh / H;
+  if (a.cu && a.batch <= kOrderSeqs) {  // sequence of rank s by length, the longest first
+    int* lens = reinterpret_cast<int*>(smem + M::kBad);
+    const int nseq = static_cast<int>(a.batch);
+    if (tid < nseq) lens[tid] = span_of(a, tid).len;
+    __syncthreads();
+    if (tid < nseq) {
+      int rank = 0;
+      for (int i = 0; i < nseq; ++i) rank += lens[i] > lens[tid] || (lens[i] == lens[tid] && i < tid);
+      if (rank == s) lens[kOrderSeqs] = tid;
+    }
+    __syncthreads();
+    s = lens[kOrderSeqs];
+  }
+  Span sp = span_of(a, s);
+  const int64_t slot0 = slot_of(a, s, sp.t0) + static_cast<int64_t>(seg) * sg.per;
+  if (sg.count > 1) {
+    sp.t0 += kC * sg.per * seg;
+    sp.len = max(0, min(sp.len - kC * sg.per * seg, kC * sg.per));
+  }
   const int nc = (sp.len + kC - 1) / kC;
 
   auto bar = [&](int b) { return sb + M::kBar + 8 * (kStages + b); };
@@ -673,8 +721,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
   const uint32_t tm = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);  // this warp's lane quarter
   const int row = 32 * (warp & 3) + lane;
-  const int64_t r = static_cast<int64_t>(slice) * 128 + row;
-  const bool row_in = r < a.dv;
+  const int r = slice * 128 + row, rows = static_cast<int>(ident ? a.dk : a.dv);
+  const bool row_in = r < rows;
   auto arrive = [&](int b) {
     tcgen05_fence_before();
     __syncwarp();
@@ -684,13 +732,29 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   if (warp < kStateWarps) {
     // ------------------------------------------------------------- state ---
     const int quarter = warp >> 2, half = quarter >> 1;
-    const int64_t sbase = ((static_cast<int64_t>(s) * a.H + h) * a.dv + (row_in ? r : 0)) * a.dk + quarter * QC;
     const int cols = static_cast<int>(min(static_cast<int64_t>(QC), max(a.dk - quarter * QC, static_cast<int64_t>(0))));
+    const int64_t at = static_cast<int64_t>(row_in ? r : 0) * a.dk + quarter * QC;  // this thread's part of a state
+    const int64_t shi = static_cast<int64_t>(s) * H + h, one = a.dv * a.dk;
+    const float* from = a.state_in ? a.state_in + shi * one : nullptr;
+    if (sg.count > 1) {
+      if (OUT) {
+        griddep_wait();  // the joined states
+        if (seg > 0 || a.state_in) from = sg.S + (shi * sg.count + seg) * one;
+      } else if (seg > 0) {
+        from = nullptr;
+      }
+    }
     uint64_t S[QC / 2];
 #pragma unroll
     for (int i = 0; i < QC; i += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (a.state_in && row_in && i < cols) v = *reinterpret_cast<const float4*>(a.state_in + sbase + i);
+      if (from && row_in && i < cols) v = *reinterpret_cast<const float4*>(from + at + i);
+      if (!OUT && from && row_in && i < cols)  // state_out may be state_in: pass 2 reads a copy
+        *reinterpret_cast<float4*>(sg.S + shi * sg.count * one + at + i) = v;
+      if (!OUT && ident) {
+        const int d = r - quarter * QC - i;
+        v = make_float4(d == 0, d == 1, d == 2, d == 3);
+      }
       S[i / 2] = pk2(v.x, v.y), S[i / 2 + 1] = pk2(v.z, v.w);
     }
     float decay = 0.0f;
@@ -742,8 +806,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       uint32_t v2[8];  // V, pairs of tokens, read while the product runs
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v2[i] = *reinterpret_cast<const uint16_t*>(vt + 2 * i * 256) |
-                static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vt + (2 * i + 1) * 256)) << 16;
+        v2[i] = !OUT && ident ? 0u
+                              : *reinterpret_cast<const uint16_t*>(vt + 2 * i * 256) |
+                                    static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vt + (2 * i + 1) * 256)) << 16;
       wait(bar(kYDone), ph, 35);
       tcgen05_fence_after();
       uint32_t marks;
@@ -791,18 +856,18 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       store_split3(tm + kTmS + 96 + 8 * quarter, 32, y);
       tmem_st_wait();
       arrive(kUsReady);
-      const int first = marks ? __ffs(marks) - 1 : 16;
-      bad[quarter * 128 + row] = marks ? 16 * quarter + first : kC;
-      replace_marked(x, 0xffffu << first & 0xffffu, 0.0f);
-      {
+      if constexpr (OUT) {
+        const int first = marks ? __ffs(marks) - 1 : 16;
+        bad[quarter * 128 + row] = marks ? 16 * quarter + first : kC;
+        replace_marked(x, 0xffffu << first & 0xffffu, 0.0f);
         uint32_t hi[8], mi[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2(x[i], hi[i], mi[i]);
         tmem_st_x8(tm + kTmU + 8 * quarter, hi);
         tmem_st_x8(tm + kTmU + 32 + 8 * quarter, mi);
+        tmem_st_wait();
+        arrive(kUoReady);
       }
-      tmem_st_wait();
-      arrive(kUoReady);
     }
     if (nc > 0) {
       wait(bar(kSDone0 + half), (nc - 1) & 1, 33);
@@ -810,18 +875,21 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
       for (int i0 = 0; i0 < QC; i0 += 16) update(i0);
     }
-    if (row_in) {
+    float* to = a.state_out + shi * one;
+    if (!OUT) to = ident ? sg.M + (shi * (sg.count - 2) + seg - 1) * a.dk * a.dk : sg.S + (shi * sg.count + seg + 1) * one;
+    if (row_in && (!OUT || seg == sg.count - 1)) {
 #pragma unroll
       for (int i = 0; i < QC; i += 4)
         if (i < cols) {
           float4 v;
           upk2(S[i / 2], v.x, v.y);
           upk2(S[i / 2 + 1], v.z, v.w);
-          *reinterpret_cast<float4*>(a.state_out + sbase + i) = v;
+          *reinterpret_cast<float4*>(to + at + i) = v;
         }
     }
   } else if (warp < kCtlWarp) {
     // ------------------------------------------------------------ output ---
+    if constexpr (OUT) {
     __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem + M::kOut) + row;
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
@@ -886,10 +954,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
     if (warp == kOutWarp && lane == 0) bulk_wait_read<0>();  // the tile stays until the last store has read it
     __syncwarp();
+    }
   } else {
     // ----------------------------------------------------------- control ---
     const int grp = h / static_cast<int>(a.H / a.G);
-    const unsigned char* img = img0 + (slot_of(a, s, sp.t0) * a.H + h) * kImgStride;
+    const unsigned char* img = img0 + (slot0 * a.H + h) * kImgStride;
     int loaded = 0;
     auto load = [&](int c) {
       if (*abort) return;
@@ -938,23 +1007,25 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       // every use of the other stage is over: its chunk's last product is done
       if (c > 0 && c + 1 < nc) {
-        wait(bar(kOaDone), ph ^ 1u, 47);
+        if constexpr (OUT) wait(bar(kOaDone), ph ^ 1u, 47);
         load(c + 1);
       }
       // Q S^T
-      if (c > 0) wait(bar(kOFree), ph ^ 1u, 42);
-      tcgen05_fence_after();
-      if (elect_one()) {
+      if constexpr (OUT) {
+        if (c > 0) wait(bar(kOFree), ph ^ 1u, 42);
+        tcgen05_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int t = 1; t >= 0; --t)
+          for (int t = 1; t >= 0; --t)
 #pragma unroll
-          for (int k = 0; k < DK; k += 16)
-            umma_f16_ts(tmem + kTmO, tmem + kTmS + (k / HC) * 96 + t * (HC / 2) + (k % HC) / 2,
-                        desc_add(kd, (k / 64) * 2 * kAtom + kAtom + (k % 64) * 2), chunk_idesc(64, false),
-                        !(t == 1 && k == 0));
-        umma_commit(bar(kOiDone));
+            for (int k = 0; k < DK; k += 16)
+              umma_f16_ts(tmem + kTmO, tmem + kTmS + (k / HC) * 96 + t * (HC / 2) + (k % HC) / 2,
+                          desc_add(kd, (k / 64) * 2 * kAtom + kAtom + (k % 64) * 2), chunk_idesc(64, false),
+                          !(t == 1 && k == 0));
+          umma_commit(bar(kOiDone));
+        }
+        __syncwarp();
       }
-      __syncwarp();
       // U = R T^T: 16 tokens j at a time meet the tokens i from theirs on
       wait(bar(kRReady), ph, 43);
       tcgen05_fence_after();
@@ -988,21 +1059,23 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       __syncwarp();
       // the scores times U
-      wait(bar(kOiRead), ph, 45);
-      wait(bar(kUoReady), ph, 46);
-      tcgen05_fence_after();
-      if (elect_one()) {
-        constexpr int kTp[3] = {1, 0, 0}, kTu[3] = {0, 1, 0};
+      if constexpr (OUT) {
+        wait(bar(kOiRead), ph, 45);
+        wait(bar(kUoReady), ph, 46);
+        tcgen05_fence_after();
+        if (elect_one()) {
+          constexpr int kTp[3] = {1, 0, 0}, kTu[3] = {0, 1, 0};
 #pragma unroll
-        for (int pr = 0; pr < 3; ++pr)
+          for (int pr = 0; pr < 3; ++pr)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ts(tmem + kTmO + 16 * kk, tmem + kTmU + 32 * kTu[pr] + 8 * kk,
-                        desc_add(td, kImgP + kTp[pr] * kPanelTerm + panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
-                        true);
-        umma_commit(bar(kOaDone));
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ts(tmem + kTmO + 16 * kk, tmem + kTmU + 32 * kTu[pr] + 8 * kk,
+                          desc_add(td, kImgP + kTp[pr] * kPanelTerm + panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
+                          true);
+          umma_commit(bar(kOaDone));
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
     // Nothing is in flight at the end of a run whose waits all came: each load and product has been waited for.
     // Otherwise wait for them here, with a limit.
@@ -1014,7 +1087,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       spin_ns(1000000);  // products take microseconds
     } else if (nc > 0) {
-      wait(bar(kOaDone), (nc - 1) & 1, 39);
+      wait(bar(OUT ? kOaDone : kSDone1), (nc - 1) & 1, 39);
     }
   }
   __syncwarp();
@@ -1026,49 +1099,152 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   }
 }
 
-template <int KA>
-cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, int64_t slots, void* ws, cudaStream_t st) {
-  unsigned char* img = static_cast<unsigned char*>(ws);
-  const int prep_smem = PrepSmem<KA>::kTotal + 1024, smem = ChainSmem<KA>::kTotal + 1024;
-  auto prep = delta_prep_kernel<KA>;
-  auto chain = delta_chain_kernel<KA>;
-  // The kernels' shared-memory limits, once per device.
-  static std::atomic<uint64_t> ready{0};
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
-    err = cudaFuncSetAttribute(prep, cudaFuncAttributeMaxDynamicSharedMemorySize, prep_smem);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(chain, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
-    if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+// First states of segments 2 .. count - 1: S_{p+1} = S_p M_p + H_p, H_p lying
+// where S_{p+1} goes. One block per 16 rows of a (sequence, head) through all
+// segments, a thread per key channel; fp32 throughout.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(128) delta_join_kernel(const DeltaArgs a, const Segments sg, int row_blocks) {
+  __shared__ float4 St[128][kJoinRows / 4];  // S_p transposed: [key channel][row]
+  const int64_t sh = blockIdx.x / row_blocks;
+  const int r0 = static_cast<int>(blockIdx.x % row_blocks) * kJoinRows, col = threadIdx.x;
+  const int dk = static_cast<int>(a.dk), nr = min(kJoinRows, static_cast<int>(a.dv) - r0);
+  const int64_t one = a.dv * a.dk;
+  float* S = sg.S + sh * sg.count * one + static_cast<int64_t>(r0) * dk;
+  const float* Mp = sg.M + sh * (sg.count - 2) * dk * dk;
+  float acc[kJoinRows];
+#pragma unroll
+  for (int r = 0; r < kJoinRows; ++r) acc[r] = r < nr && col < dk ? S[one + r * dk + col] : 0.0f;
+  for (int p = 1; p + 1 < sg.count; ++p, Mp += dk * dk) {
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kJoinRows; r += 4) St[col][r / 4] = make_float4(acc[r], acc[r + 1], acc[r + 2], acc[r + 3]);
+    __syncthreads();
+    float* next = S + (p + 1) * one;
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) acc[r] = r < nr && col < dk ? next[r * dk + col] : 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < dk; ++k) {
+      const float m = col < dk ? Mp[k * dk + col] : 0.0f;
+#pragma unroll
+      for (int r = 0; r < kJoinRows; r += 4) {
+        const float4 v = St[k][r / 4];
+        acc[r] = fmaf(v.x, m, acc[r]);
+        acc[r + 1] = fmaf(v.y, m, acc[r + 1]);
+        acc[r + 2] = fmaf(v.z, m, acc[r + 2]);
+        acc[r + 3] = fmaf(v.w, m, acc[r + 3]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r)
+      if (r < nr && col < dk) next[r * dk + col] = acc[r];
   }
-  const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
-  prep<<<static_cast<unsigned>(slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  const int slices = static_cast<int>((a.dv + 127) / 128);
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch * a.H * slices));
-  cfg.blockDim = dim3(kChainThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chain, maps, a, static_cast<const unsigned char*>(img), slices);
 }
 
 int64_t chunk_slots(int64_t batch, int64_t L, bool packed) {
   return packed ? L / kC + batch : batch * ((L + kC - 1) / kC);
 }
 
+// Segments of a walk of nc chunks with `units` (sequence, head, slice) on
+// `sms` SMs, in units of a chunk's time (3.4 us): one walk takes nc for each
+// wave of units; pass 1 walks at 0.9, and the extra launches and the join cost
+// about 8 chunks and half a chunk a segment. Lengths of packed sequences are
+// known on the device alone: one walk each.
+int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int sms, int* per) {
+  auto waves = [sms](int64_t blocks) { return static_cast<double>((blocks + sms - 1) / sms); };
+  const double single = static_cast<double>(nc) * waves(units);
+  double best = 0.85 * single;
+  int count = 1;
+  *per = static_cast<int>(nc);
+  for (int64_t p = 2; p <= 64 && 4 * p <= nc && units * p <= 64 * sms; ++p) {
+    const int64_t len = (nc + p - 1) / p;
+    if ((nc + len - 1) / len != p) continue;
+    const double cost = static_cast<double>(len) * (0.9 * waves(units * (p - 1) + seq_heads * (p - 2)) + waves(units * p)) +
+                        8.0 + 0.5 * static_cast<double>(p);
+    if (cost < best) best = cost, count = static_cast<int>(p), *per = static_cast<int>(len);
+  }
+  return count;
+}
+
+struct ChunkPlan {
+  int64_t slots;
+  int slices, count, per;
+  size_t S, M, bytes;  // offsets of the segments' states behind the operand tiles, and the end
+};
+ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv, bool packed) {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  else cudaGetLastError();  // no device: the default SM count
+  ChunkPlan p{};
+  p.slots = chunk_slots(batch, L, packed);
+  p.slices = static_cast<int>((dv + 127) / 128);
+  const int64_t nc = (L + kC - 1) / kC;
+  p.count = packed ? 1 : choose_segments(nc, batch * H * p.slices, batch * H, sms > 0 ? sms : 148, &p.per);
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  p.S = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
+  p.M = p.bytes = p.S;
+  if (p.count > 1) {
+    p.M = up(p.S + static_cast<size_t>(batch * H * p.count * dv * dk) * 4);
+    p.bytes = up(p.M + static_cast<size_t>(batch * H * (p.count - 2) * dk * dk) * 4);
+  }
+  return p;
+}
+
+template <int KA, bool OUT>
+cudaError_t launch_chain(const ChunkMaps& maps, const DeltaArgs& a, const unsigned char* img, const ChunkPlan& p,
+                         const Segments& sg, int64_t blocks, bool after_prep, cudaStream_t st) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kChainThreads);
+  cfg.dynamicSmemBytes = ChainSmem<KA>::kTotal + 1024;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = after_prep ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, delta_chain_kernel<KA, OUT>, maps, a, img, p.slices, sg);
+}
+
+template <int KA>
+cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkPlan& p, void* ws, cudaStream_t st) {
+  unsigned char* img = static_cast<unsigned char*>(ws);
+  const int prep_smem = PrepSmem<KA>::kTotal + 1024, smem = ChainSmem<KA>::kTotal + 1024;
+  auto prep = delta_prep_kernel<KA>;
+  // The kernels' shared-memory limits, once per device.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    err = cudaFuncSetAttribute(prep, kAttr, prep_smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false>, kAttr, smem);
+    if (err != cudaSuccess) return err;
+    if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
+  }
+  const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
+  prep<<<static_cast<unsigned>(p.slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  const int64_t bh = a.batch * a.H, units = bh * p.slices;
+  Segments sg{p.count, p.per, nullptr, nullptr};
+  if (p.count == 1) return launch_chain<KA, true>(maps, a, img, p, sg, units, true, st);
+  sg.S = reinterpret_cast<float*>(img + p.S), sg.M = reinterpret_cast<float*>(img + p.M);
+  err = launch_chain<KA, false>(maps, a, img, p, sg, units * (p.count - 1) + bh * (p.count - 2), true, st);
+  if (err != cudaSuccess) return err;
+  if (p.count > 2) {
+    const int rb = static_cast<int>((a.dv + kJoinRows - 1) / kJoinRows);
+    delta_join_kernel<<<static_cast<unsigned>(bh * rb), 128, 0, st>>>(a, sg, rb);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  }
+  return launch_chain<KA, true>(maps, a, img, p, sg, units * p.count, false, st);
+}
+
 }  // namespace
 
-size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, bool packed) {
-  return static_cast<size_t>(chunk_slots(batch, L, packed)) * static_cast<size_t>(H) * kImgStride;
+size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv, bool packed) {
+  return chunk_plan(batch, L, H, dk, dv, packed).bytes;
 }
 
 cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st) {
@@ -1086,8 +1262,8 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st) {
       !map4(&m.v, a.v, a.dv, a.H, a.v_tok, a.v_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !map4(&m.out, a.out, a.dv, a.H, a.o_tok, a.o_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  const int64_t slots = chunk_slots(a.batch, a.L, packed);
-  return a.dk > 64 ? launch_chunk<2>(m, a, slots, ws, st) : launch_chunk<1>(m, a, slots, ws, st);
+  const ChunkPlan p = chunk_plan(a.batch, a.L, a.H, a.dk, a.dv, packed);
+  return a.dk > 64 ? launch_chunk<2>(m, a, p, ws, st) : launch_chunk<1>(m, a, p, ws, st);
 }
 
 }  // namespace ssm
