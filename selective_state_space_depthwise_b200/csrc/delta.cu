@@ -242,6 +242,7 @@ ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, cons
   a->cu = nullptr, a->index = nullptr, a->num_states = d->batch;
   a->scale = d->scale != 0.0f ? d->scale : 1.0f / sqrtf(static_cast<float>(d->d_key));
   a->l2norm = d->qk_l2norm;
+  a->two16 = 65536u;
   a->err = nullptr;
   return SSM_OK;
 }

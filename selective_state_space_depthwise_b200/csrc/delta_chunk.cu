@@ -30,8 +30,8 @@
 //
 // Precision. q, k and v are bf16 and enter exactly; the key norms, decays and
 // beta are fp32 factors of rows and columns, never folded into a bf16 operand.
-// S, R, U and T are fp32 and go to the tensor cores as three bf16 terms (the
-// top 8 bits, the next 8, the last 8 of the significand: exact), as many
+// S, R, U and T are fp32 and go to the tensor cores as three bf16 terms (their
+// sum is exact), as many
 // products as pairs of terms above 2^-24. Only the output's own product takes
 // two terms (2^-16, against its rounding to bf16). The tensor core adds into
 // fp32 accumulators with truncation, so the state itself is added up in fp32
@@ -131,39 +131,51 @@ struct Waiter {
   }
 };
 
-// A pair of values as three packed bf16 pairs whose sum is exact: 8 bits of the significand each.
-__device__ __forceinline__ void split3(uint64_t x, uint32_t& h, uint32_t& m, uint32_t& l) {
+// bf16 in the low half of w, as a float: times 65536 on the FMA pipe. The
+// factor comes from memory (2^16, kept from the compiler), since a shift would
+// go to the integer pipe, which the walk's conversions fill.
+struct Shifter {
+  uint32_t by;
+  __device__ __forceinline__ float low(uint32_t w) const { return __uint_as_float(w * by); }
+};
+__device__ __forceinline__ float high_bf16(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// A pair of values as three packed bf16 pairs whose sum is exact: each rounding
+// leaves at most 16, then 8 bits of the significand. Five integer-pipe
+// instructions a pair; with masks and byte permutes instead of the conversions
+// and the product, seven.
+__device__ __forceinline__ void split3(const Shifter& sh, uint64_t x, uint32_t& h, uint32_t& m, uint32_t& l) {
   const uint64_t minus = pk2(-1.0f, -1.0f);
   float a, b;
   upk2(x, a, b);
-  h = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-  const uint64_t r = ffma2(pk2(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
-                               __uint_as_float(__float_as_uint(b) & 0xffff0000u)), minus, x);
+  h = pack_bf16(a, b);
+  const uint64_t r = ffma2(pk2(sh.low(h), high_bf16(h)), minus, x);
   upk2(r, a, b);
-  m = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-  const uint64_t s = ffma2(pk2(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
-                               __uint_as_float(__float_as_uint(b) & 0xffff0000u)), minus, r);
+  m = pack_bf16(a, b);
+  const uint64_t s = ffma2(pk2(sh.low(m), high_bf16(m)), minus, r);
   upk2(s, a, b);
-  l = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  l = pack_bf16(a, b);
 }
-// As two: the top 8 bits, and the rest rounded.
-__device__ __forceinline__ void split2(uint64_t x, uint32_t& h, uint32_t& m) {
+// As two: 2^-18 of the value is left out.
+__device__ __forceinline__ void split2(const Shifter& sh, uint64_t x, uint32_t& h, uint32_t& m) {
   float a, b;
   upk2(x, a, b);
-  h = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-  const uint64_t r = ffma2(pk2(__uint_as_float(__float_as_uint(a) & 0xffff0000u),
-                               __uint_as_float(__float_as_uint(b) & 0xffff0000u)), pk2(-1.0f, -1.0f), x);
+  h = pack_bf16(a, b);
+  const uint64_t r = ffma2(pk2(sh.low(h), high_bf16(h)), pk2(-1.0f, -1.0f), x);
   upk2(r, a, b);
-  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-  m = *reinterpret_cast<const uint32_t*>(&p);
+  m = pack_bf16(a, b);
 }
 __device__ __forceinline__ uint64_t pk2u(uint32_t a, uint32_t b) { return pk2(__uint_as_float(a), __uint_as_float(b)); }
 
 // 16 values of a row as three terms at columns col + t * stride of A-operand tensor memory.
-__device__ __forceinline__ void store_split3(uint32_t col, uint32_t stride, const uint64_t (&x)[8]) {
+__device__ __forceinline__ void store_split3(const Shifter& sh, uint32_t col, uint32_t stride, const uint64_t (&x)[8]) {
   uint32_t h[8], m[8], l[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) split3(x[i], h[i], m[i], l[i]);
+  for (int i = 0; i < 8; ++i) split3(sh, x[i], h[i], m[i], l[i]);
   tmem_st_x8(col, h);
   tmem_st_x8(col + stride, m);
   tmem_st_x8(col + 2 * stride, l);
@@ -292,6 +304,7 @@ __global__ void __launch_bounds__(128, 4)
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(smem);
   const int pt = threadIdx.x, lane = pt & 31;
+  const Shifter sh{a.two16};
   const int warp = __shfl_sync(0xffffffffu, pt >> 5, 0);
   const int rep = static_cast<int>(a.H / a.G);
   const int set = static_cast<int>(blockIdx.x) % head_sets;
@@ -451,7 +464,7 @@ __global__ void __launch_bounds__(128, 4)
         if (is_q) {
           uint32_t hi[4], mi[4];
 #pragma unroll
-          for (int z = 0; z < 4; ++z) split2(pk2(f[2 * z], f[2 * z + 1]), hi[z], mi[z]);
+          for (int z = 0; z < 4; ++z) split2(sh, pk2(f[2 * z], f[2 * z + 1]), hi[z], mi[z]);
           unsigned char* p = img + kImgP + panel_piece(i, j >> 3);
           *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(p + kPanelTerm) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
@@ -560,8 +573,8 @@ __global__ void __launch_bounds__(128, 4)
         const int j = 8 * j8 + e;
         const float4 w = *reinterpret_cast<const float4*>(As + i * kALd + j);
         const float4 b4 = *reinterpret_cast<const float4*>(beta + j);
-        split3(pk2(j <= i ? w.x * b4.x : 0.0f, j + 1 <= i ? w.y * b4.y : 0.0f), hi[e / 2], mi[e / 2], lo[e / 2]);
-        split3(pk2(j + 2 <= i ? w.z * b4.z : 0.0f, j + 3 <= i ? w.w * b4.w : 0.0f), hi[e / 2 + 1], mi[e / 2 + 1],
+        split3(sh, pk2(j <= i ? w.x * b4.x : 0.0f, j + 1 <= i ? w.y * b4.y : 0.0f), hi[e / 2], mi[e / 2], lo[e / 2]);
+        split3(sh, pk2(j + 2 <= i ? w.z * b4.z : 0.0f, j + 3 <= i ? w.w * b4.w : 0.0f), hi[e / 2 + 1], mi[e / 2 + 1],
                lo[e / 2 + 1]);
       }
       unsigned char* p = img + panel_piece(i, j8);
@@ -653,6 +666,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const uint32_t sb = smem_u32(smem);
   const int tid = threadIdx.x, lane = tid & 31;
+  const Shifter sh{a.two16};
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // This block's sequence, head, rows and segment; `ident`: it walks the identity.
   const int H = static_cast<int>(a.H);
@@ -670,8 +684,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       seg = unit % (sg.count - 1), unit /= sg.count - 1;
     }
   }
-  const int slice = unit % slices, sh = unit / slices, h = sh % H;
-  int s = sh / H;
+  const int slice = unit % slices, seq_head = unit / slices, h = seq_head % H;
+  int s = seq_head / H;
   if (a.cu && a.batch <= kOrderSeqs) {  // sequence of rank s by length, the longest first
     int* lens = reinterpret_cast<int*>(smem + M::kBad);
     const int nseq = static_cast<int>(a.batch);
@@ -795,7 +809,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         uint64_t x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = S[8 * b + i];
-        store_split3(tm_s + 8 * b, HC / 2, x);
+        store_split3(sh, tm_s + 8 * b, HC / 2, x);
         tmem_st_wait();
         arrive(kSReady0 + b);
       }
@@ -803,12 +817,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       wait(full(c), (c >> 1) & 1, 34);
       decay = cf.decay;
       const unsigned char* vt = stage + M::kV + row * 2 + 16 * quarter * 256;
-      uint32_t v2[8];  // V, pairs of tokens, read while the product runs
+      uint32_t v[16];  // V, read while the product runs
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v2[i] = !OUT && ident ? 0u
-                              : *reinterpret_cast<const uint16_t*>(vt + 2 * i * 256) |
-                                    static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vt + (2 * i + 1) * 256)) << 16;
+      for (int i = 0; i < 16; ++i)
+        v[i] = !OUT && ident ? 0u : *reinterpret_cast<const uint16_t*>(vt + i * 256);
       wait(bar(kYDone), ph, 35);
       tcgen05_fence_after();
       uint32_t marks;
@@ -820,9 +832,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 e4 = *reinterpret_cast<const float4*>(cf.neg + 16 * quarter + i);
-          const uint32_t va = v2[i / 2], vb = v2[i / 2 + 1];
-          x[i / 2] = ffma2(pk2(e4.x, e4.y), pk2u(d[i], d[i + 1]), pk2u(va << 16, va & 0xffff0000u));
-          x[i / 2 + 1] = ffma2(pk2(e4.z, e4.w), pk2u(d[i + 2], d[i + 3]), pk2u(vb << 16, vb & 0xffff0000u));
+          x[i / 2] = ffma2(pk2(e4.x, e4.y), pk2u(d[i], d[i + 1]), pk2(sh.low(v[i]), sh.low(v[i + 1])));
+          x[i / 2 + 1] = ffma2(pk2(e4.z, e4.w), pk2u(d[i + 2], d[i + 3]), pk2(sh.low(v[i + 2]), sh.low(v[i + 3])));
         }
         if (n < kC) {
           const int left = n - 16 * quarter;  // tokens of the sequence from here
@@ -830,7 +841,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         marks = not_finite(x);
         replace_marked(x, marks, 0.0f);
-        store_split3(tm + kTmDelta + 8 * quarter, 32, x);
+        store_split3(sh, tm + kTmDelta + 8 * quarter, 32, x);
       }
       tmem_st_wait();
       arrive(kRReady);
@@ -853,7 +864,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         y[i / 2 + 1] = fmul2(x[i / 2 + 1], pk2(e4.z, e4.w));
       }
       replace_marked(y, marks, __uint_as_float(0x7fffffffu));
-      store_split3(tm + kTmS + 96 + 8 * quarter, 32, y);
+      store_split3(sh, tm + kTmS + 96 + 8 * quarter, 32, y);
       tmem_st_wait();
       arrive(kUsReady);
       if constexpr (OUT) {
@@ -862,7 +873,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         replace_marked(x, 0xffffu << first & 0xffffu, 0.0f);
         uint32_t hi[8], mi[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) split2(x[i], hi[i], mi[i]);
+        for (int i = 0; i < 8; ++i) split2(sh, x[i], hi[i], mi[i]);
         tmem_st_x8(tm + kTmU + 8 * quarter, hi);
         tmem_st_x8(tm + kTmU + 32 + 8 * quarter, mi);
         tmem_st_wait();

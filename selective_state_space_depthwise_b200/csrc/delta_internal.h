@@ -20,6 +20,7 @@ struct DeltaArgs {
   int64_t q_tok, q_seq, k_tok, k_seq, v_tok, v_seq, o_tok, o_seq, gb_tok, gb_seq;
   float scale;
   int l2norm;
+  uint32_t two16;  // 65536, a value the compiler does not know
   int* err;
 };
 
