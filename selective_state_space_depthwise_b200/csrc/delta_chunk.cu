@@ -38,8 +38,10 @@
 // registers, and the accumulators hold one chunk's contribution at a time.
 //
 // Values that are not finite: a product with a zero would spread them to tokens
-// before theirs, so the state warps take them out of the operands, mark the
-// first such token of each row, and the output warps write NaN from there on.
+// before theirs. Those of a token's k, g and beta (found by the prep) and of v
+// (found while the walk waits for a product) are taken out of the operands; the
+// state gets a NaN for them, and the outputs are NaN from the first such token
+// on. A state that is not finite makes its row's outputs so by itself.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -70,7 +72,8 @@ struct Coef {
   float ec[kC];  // e^{G_C - G_j} / |k_j|, 0 behind the sequence: scales U into the state
   float oq[kC];  // scale e^{G_i} / |q_i|: scales Q S^T
   float decay;   // e^{G_C}
-  float pad[3];
+  uint32_t bad[2];  // bit j: token j's k, g or beta is not finite
+  float pad;
 };
 constexpr int kImgP = 3 * kPanelTerm, kImgCoef = 5 * kPanelTerm;
 constexpr int kImgBytes = kImgCoef + static_cast<int>(sizeof(Coef));
@@ -183,35 +186,32 @@ __device__ __forceinline__ void store_split3(const Shifter& sh, uint32_t col, ui
 
 __device__ __forceinline__ int sw128(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 
-// Bit i set where value i of the 16 is not finite.
+// Bit i set where value i of the 16 is not finite. Nearly always none in the
+// whole warp, which one vote tells without a divergent branch.
 __device__ __forceinline__ uint32_t not_finite(const uint64_t (&x)[8]) {
-  uint64_t s = 0;
+  uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = ffma2(x[i], 0ull, s);
+  for (int i = 0; i < 8; i += 2) s0 = ffma2(x[i], 0ull, s0), s1 = ffma2(x[i + 1], 0ull, s1);
   float a, b;
-  upk2(s, a, b);
+  upk2(fadd2(s0, s1), a, b);
   uint32_t bits = 0;
-  if (!(a + b == 0.0f)) {
+  if (__any_sync(0xffffffffu, !(a + b == 0.0f))) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       upk2(x[i], a, b);
       bits |= (fabsf(a) <= 3.4028235e38f ? 0u : 1u << (2 * i)) | (fabsf(b) <= 3.4028235e38f ? 0u : 2u << (2 * i));
     }
   }
-  __syncwarp();
   return bits;
 }
 // Puts `to` in the place of the marked ones.
 __device__ __forceinline__ void replace_marked(uint64_t (&x)[8], uint32_t marks, float to) {
-  if (marks) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float a, b;
-      upk2(x[i], a, b);
-      x[i] = pk2(marks >> (2 * i) & 1 ? to : a, marks >> (2 * i + 1) & 1 ? to : b);
-    }
+  for (int i = 0; i < 8; ++i) {
+    float a, b;
+    upk2(x[i], a, b);
+    x[i] = pk2(marks >> (2 * i) & 1 ? to : a, marks >> (2 * i + 1) & 1 ? to : b);
   }
-  __syncwarp();
 }
 
 struct ChunkMaps {
@@ -402,7 +402,8 @@ __global__ void __launch_bounds__(128, 4)
   }
   wait(full, 0, 31);
   float rn = 1.0f;  // 1 / |row|
-  if (a.l2norm) {
+  bool k_bad = false;
+  if (a.l2norm || !is_q) {
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll 1
     for (int t = 0; t < KA; ++t) {
@@ -418,7 +419,8 @@ __global__ void __launch_bounds__(128, 4)
         }
       }
     }
-    rn = rsqrtf(s0 + s1 + kL2Eps);
+    k_bad = !(s0 + s1 <= 3.4028235e38f);
+    if (a.l2norm) rn = rsqrtf(s0 + s1 + kL2Eps);
   }
   if (!is_q) rk[i] = rn;
   wait(done, 0, 32);
@@ -443,6 +445,9 @@ __global__ void __launch_bounds__(128, 4)
       cf->neg[i] = -eg * rn;
       cf->ec[i] = i < n ? ex2_approx((Ghi[kC - 1] - Gi) + (Glo[kC - 1] - Gl)) * rn : 0.0f;
       if (i == kC - 1) cf->decay = eg;
+      const bool bad = i < n && (k_bad || !(fabsf(Gi) <= 3.4028235e38f) || !(fabsf(beta[i]) <= 3.4028235e38f));
+      const uint32_t bits = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) cf->bad[warp] = bits;
     }
     {  // column factors of block row b, columns j < 16 b
       const int b = pt < 48 ? 3 : pt < 96 ? 2 : 1, j = pt < 48 ? pt : pt < 96 ? pt - 64 : pt - 96;
@@ -598,17 +603,16 @@ __global__ void __launch_bounds__(128, 4)
 }
 
 // ------------------------------------------------------------------- walk ---
-// One CTA per (sequence, head, 128 rows of d_value), 21 warps:
-//   warps 0-15  state: hold S (a thread: one row, a quarter of the key
-//               channels), form the A operands between the products. Four of
-//               them on each quarter of the SM keep its integer pipe busy (a
-//               pair of values in three terms takes 14 of its cycles) over the
-//               latencies of tensor memory, which two do not;
-//   warps 16-19 output: scale Q S^T where it lies, take the sum with the
-//               scores' product from there, round and store;
-//   warp 20     one thread issues the loads (two chunks in flight) and every MMA.
-constexpr int kStateWarps = 16, kOutWarp = 16, kCtlWarp = 20;
-constexpr int kChainThreads = 32 * 21;
+// One CTA per (sequence, head, 128 rows of d_value), 17 warps:
+//   warps 0-15  hold S (a thread: one row, a quarter of the key channels), form
+//               the A operands between the products, and in their waits for
+//               the products the outputs (a thread: one row, 16 tokens): Q S^T
+//               is scaled where it lies, the scores' product adds to it there,
+//               and the sum is rounded and stored a chunk later;
+//   warp 16     one thread issues the loads (two chunks in flight) and every MMA.
+// (Output warps of their own, 21 in all, leave 80 registers a thread: spills.)
+constexpr int kStateWarps = 16, kCtlWarp = 16;
+constexpr int kChainThreads = 32 * 17;
 constexpr int kStages = 2;
 
 // Tensor memory, 512 columns.
@@ -624,20 +628,20 @@ struct ChainSmem {
   static constexpr int kV = kKQ;              // [token][128]
   static constexpr int kImg = kV + kC * 256;
   static constexpr int kStage = (kImg + kImgStride + 1023) / 1024 * 1024;
-  static constexpr int kOut = kStages * kStage;  // [token][128] bf16
-  static constexpr int kBad = kOut + kC * 256;   // int [4][128]
+  static constexpr int kOut = kStages * kStage;      // two chunks of [token][128] bf16
+  static constexpr int kBad = kOut + 2 * kC * 256;   // int [4][128]
   static constexpr int kBar = kBad + 4 * 128 * 4;
-  static constexpr int kMisc = kBar + (kStages + 14) * 8;  // TMEM address, abort flag
+  static constexpr int kMisc = kBar + (kStages + 16) * 8;  // TMEM address, abort flag
   static constexpr int kTotal = kMisc + 16;
   static_assert(kTotal + 1024 <= 232448, "227 KB of shared memory");
   static constexpr uint32_t kTx = static_cast<uint32_t>(kImg + kImgBytes);
 };
 
 enum Bar {  // after the stages' full barriers; each completes once a chunk
-  kSReady0, kSReady1, kYDone, kOiDone, kRReady, kUDone, kUsReady, kSDone0, kSDone1, kUoReady, kOiRead, kOaDone, kOFree,
-  kNumNamed
+  kSReady0, kSReady1, kSReady2, kSReady3, kYDone, kOiDone, kRReady, kUDone, kUsReady, kSDone0, kSDone1, kUoReady, kOiRead,
+  kOaDone, kOFree, kNumNamed
 };
-static_assert(kNumNamed <= 14, "barrier count");
+static_assert(kNumNamed <= 15, "barrier count");
 
 // A long sequence with few heads leaves most SMs idle, so it may be walked in
 // `count` segments of `per` chunks at once. The state is linear in the one
@@ -715,7 +719,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 
   if (tid == 32 * kCtlWarp) {
     for (int i = 0; i < kStages; ++i) mbar_init(sb + M::kBar + 8 * i, 1);
-    const uint32_t counts[kNumNamed] = {16, 16, 1, 1, 16, 1, 16, 1, 1, 16, 4, 1, 4};
+    const uint32_t counts[kNumNamed] = {8, 8, 8, 8, 1, 1, 16, 1, 16, 1, 1, 16, 16, 1, 16};
     for (int i = 0; i < kNumNamed; ++i) mbar_init(bar(i), counts[i]);
     *abort = 0;
     mbar_fence_init();
@@ -781,6 +785,42 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) S[i0 / 2 + i] = ffma2(dd, S[i0 / 2 + i], pk2u(d[2 * i], d[2 * i + 1]));
     };
+    // Rounds and stores this thread's 16 tokens of chunk c, once the scores' product is in.
+    auto store_chunk = [&](int c) {
+      const int n = min(kC, sp.len - kC * c), t0 = 16 * quarter;
+      __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem + M::kOut + (c & 1) * kC * 256) + t0 * 128 + row;
+      wait(bar(kOaDone), c & 1, 39);
+      tcgen05_fence_after();
+      uint32_t d[16];
+      tmem_ld_x16(tm + kTmO + t0, d);
+      tmem_ld_wait();
+      arrive(kOFree);
+      const int first = min(min(bad[row], bad[128 + row]), min(bad[256 + row], bad[384 + row])) - t0;
+      if (__any_sync(0xffffffffu, first < 16)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i >= first) d[i] = 0x7fffffffu;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) tile[i * 128] = __float2bfloat16_rn(__uint_as_float(d[i]));
+      // A tile store per 16 tokens; it leaves out channels past d_value and tokens past L. The last tokens of a
+      // packed sequence may end inside one: those rows are written one by one.
+      const bool issuer = (warp & 3) == 0 && lane == 0;
+      if (!a.cu || n >= t0 + 16) {
+        fence_proxy_async_smem();
+        if (issuer) bulk_wait_read<0>();  // the last chunk's store has read its half of the tiles
+        named_bar_sync(1 + quarter, 128);
+        if (issuer) {
+          tma_store_4d(&maps.out, sb + M::kOut + (c & 1) * kC * 256 + t0 * 256, 128 * slice, h, sp.t0 + kC * c + t0,
+                       sp.seq);
+          bulk_commit();
+        }
+      } else if (row_in) {
+        __nv_bfloat16* op = a.out + (static_cast<int64_t>(sp.t0) + kC * c + t0) * a.o_tok + h * a.dv + r;
+        for (int t = 0; t0 + t < n; ++t) op[t * a.o_tok] = tile[t * 128];
+      }
+      __syncwarp();
+    };
     const uint32_t tm_s = tm + kTmS + half * 96 + (quarter & 1) * (QC / 2);  // its columns of S's terms
     const uint32_t tm_y = tm + kTmY + 16 * quarter;                          // its 16 tokens
 #pragma unroll 1
@@ -811,19 +851,31 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int i = 0; i < 8; ++i) x[i] = S[8 * b + i];
         store_split3(sh, tm_s + 8 * b, HC / 2, x);
         tmem_st_wait();
-        arrive(kSReady0 + b);
+        arrive(kSReady0 + half * KA + b);
       }
+      if (OUT && c > 0) store_chunk(c - 1);
       // R = V - e^G Y
       wait(full(c), (c >> 1) & 1, 34);
       decay = cf.decay;
       const unsigned char* vt = stage + M::kV + row * 2 + 16 * quarter * 256;
-      uint32_t v[16];  // V, read while the product runs
+      // V, read while the product runs, and what must stay out of R: `marks`, tokens that are not finite, and `drop`,
+      // those and the tokens behind the sequence.
+      uint64_t v[8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        v[i] = !OUT && ident ? 0u : *reinterpret_cast<const uint16_t*>(vt + i * 256);
+      for (int i = 0; i < 8; ++i) {
+        v[i] = 0;
+        if (OUT || !ident)
+          v[i] = pk2(sh.low(*reinterpret_cast<const uint16_t*>(vt + 2 * i * 256)),
+                     sh.low(*reinterpret_cast<const uint16_t*>(vt + (2 * i + 1) * 256)));
+      }
+      const int left = n - 16 * quarter;
+      const uint32_t real = left >= 16 ? 0xffffu : left <= 0 ? 0u : 0xffffu >> (16 - left);
+      const uint32_t marks = (not_finite(v) | cf.bad[half] >> (16 * (quarter & 1))) & real;
+      const bool any_marks = __any_sync(0xffffffffu, marks != 0u);
+      const uint32_t drop = marks | (~real & 0xffffu);
+      const bool any_drop = any_marks || real != 0xffffu;
       wait(bar(kYDone), ph, 35);
       tcgen05_fence_after();
-      uint32_t marks;
       {
         uint32_t d[16];
         uint64_t x[8];
@@ -832,19 +884,34 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 e4 = *reinterpret_cast<const float4*>(cf.neg + 16 * quarter + i);
-          x[i / 2] = ffma2(pk2(e4.x, e4.y), pk2u(d[i], d[i + 1]), pk2(sh.low(v[i]), sh.low(v[i + 1])));
-          x[i / 2 + 1] = ffma2(pk2(e4.z, e4.w), pk2u(d[i + 2], d[i + 3]), pk2(sh.low(v[i + 2]), sh.low(v[i + 3])));
+          x[i / 2] = ffma2(pk2(e4.x, e4.y), pk2u(d[i], d[i + 1]), v[i / 2]);
+          x[i / 2 + 1] = ffma2(pk2(e4.z, e4.w), pk2u(d[i + 2], d[i + 3]), v[i / 2 + 1]);
         }
-        if (n < kC) {
-          const int left = n - 16 * quarter;  // tokens of the sequence from here
-          replace_marked(x, left >= 16 ? 0u : left <= 0 ? 0xffffu : 0xffffu << left & 0xffffu, 0.0f);
-        }
-        marks = not_finite(x);
-        replace_marked(x, marks, 0.0f);
+        if (any_drop) replace_marked(x, drop, 0.0f);
         store_split3(sh, tm + kTmDelta + 8 * quarter, 32, x);
       }
       tmem_st_wait();
       arrive(kRReady);
+      if constexpr (OUT) {  // scale Q S^T
+        wait(bar(kOiDone), ph, 38);
+        tcgen05_fence_after();
+        uint32_t d[16];
+        tmem_ld_x16(tm + kTmO + 16 * quarter, d);
+        float4 es[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) es[i] = *reinterpret_cast<const float4*>(cf.oq + 16 * quarter + 4 * i);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d[4 * i] = __float_as_uint(__uint_as_float(d[4 * i]) * es[i].x);
+          d[4 * i + 1] = __float_as_uint(__uint_as_float(d[4 * i + 1]) * es[i].y);
+          d[4 * i + 2] = __float_as_uint(__uint_as_float(d[4 * i + 2]) * es[i].z);
+          d[4 * i + 3] = __float_as_uint(__uint_as_float(d[4 * i + 3]) * es[i].w);
+        }
+        tmem_st_x16(tm + kTmO + 16 * quarter, d);
+        tmem_st_wait();
+        arrive(kOiRead);
+      }
       // U: scaled into the state's product, plain into the output's
       wait(bar(kUDone), ph, 36);
       tcgen05_fence_after();
@@ -855,22 +922,21 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = pk2u(d[2 * i], d[2 * i + 1]);
-      }
-      marks |= not_finite(x);
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 e4 = *reinterpret_cast<const float4*>(cf.ec + 16 * quarter + i);
-        y[i / 2] = fmul2(x[i / 2], pk2(e4.x, e4.y));
-        y[i / 2 + 1] = fmul2(x[i / 2 + 1], pk2(e4.z, e4.w));
+        for (int i = 0; i < 4; ++i) {
+          const float4 e4 = *reinterpret_cast<const float4*>(cf.ec + 16 * quarter + 4 * i);
+          y[2 * i] = fmul2(x[2 * i], pk2(e4.x, e4.y));
+          y[2 * i + 1] = fmul2(x[2 * i + 1], pk2(e4.z, e4.w));
+        }
       }
-      replace_marked(y, marks, __uint_as_float(0x7fffffffu));
+      if (any_marks) replace_marked(y, marks, __uint_as_float(0x7fffffffu));
       store_split3(sh, tm + kTmS + 96 + 8 * quarter, 32, y);
       tmem_st_wait();
       arrive(kUsReady);
       if constexpr (OUT) {
         const int first = marks ? __ffs(marks) - 1 : 16;
         bad[quarter * 128 + row] = marks ? 16 * quarter + first : kC;
-        replace_marked(x, 0xffffu << first & 0xffffu, 0.0f);
+        if (any_marks) replace_marked(x, 0xffffu << first & 0xffffu, 0.0f);
         uint32_t hi[8], mi[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2(sh, x[i], hi[i], mi[i]);
@@ -881,6 +947,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
     }
     if (nc > 0) {
+      if constexpr (OUT) store_chunk(nc - 1);
       wait(bar(kSDone0 + half), (nc - 1) & 1, 33);
       tcgen05_fence_after();
 #pragma unroll
@@ -898,74 +965,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
           *reinterpret_cast<float4*>(to + at + i) = v;
         }
     }
-  } else if (warp < kCtlWarp) {
-    // ------------------------------------------------------------ output ---
-    if constexpr (OUT) {
-    __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem + M::kOut) + row;
-#pragma unroll 1
-    for (int c = 0; c < nc; ++c) {
-      const uint32_t ph = c & 1;
-      const Coef& cf = *reinterpret_cast<const Coef*>(smem + ph * M::kStage + M::kImg + kImgCoef);
-      const int n = min(kC, sp.len - kC * c);
-      wait(full(c), (c >> 1) & 1, 37);
-      wait(bar(kOiDone), ph, 38);
-      tcgen05_fence_after();
-#pragma unroll 1
-      for (int u = 0; u < kC; u += 16) {
-        uint32_t d[16];
-        tmem_ld_x16(tm + kTmO + u, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 q4 = *reinterpret_cast<const float4*>(cf.oq + u + i);
-          const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-          for (int z = 0; z < 4; ++z) d[i + z] = __float_as_uint(__uint_as_float(d[i + z]) * qs[z]);
-        }
-        tmem_st_x16(tm + kTmO + u, d);
-      }
-      tmem_st_wait();
-      arrive(kOiRead);
-      wait(bar(kOaDone), ph, 39);
-      tcgen05_fence_after();
-      const int first = min(min(bad[row], bad[128 + row]), min(bad[256 + row], bad[384 + row]));
-      if (c > 0) {  // the last chunk's tile has been read
-        if (warp == kOutWarp && lane == 0) bulk_wait_read<0>();
-        named_bar_sync(1, 128);
-      }
-#pragma unroll 1
-      for (int u = 0; u < kC; u += 16) {
-        uint32_t d[16];
-        tmem_ld_x16(tm + kTmO + u, d);
-        tmem_ld_wait();
-        if (u == kC - 16) arrive(kOFree);
-        if (first < u + 16) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (u + i >= first) d[i] = 0x7fffffffu;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) tile[(u + i) * 128] = __float2bfloat16_rn(__uint_as_float(d[i]));
-      }
-      // One tile store writes the chunk; it leaves out channels past d_value and tokens past L. The last tokens of
-      // a packed sequence end inside the tile: rows are written one by one.
-      if (!a.cu || n == kC) {
-        fence_proxy_async_smem();
-        named_bar_sync(1, 128);
-        if (warp == kOutWarp && lane == 0) {
-          tma_store_4d(&maps.out, sb + M::kOut, 128 * slice, h, sp.t0 + kC * c, sp.seq);
-          bulk_commit();
-        }
-      } else if (row_in) {
-        __nv_bfloat16* op = a.out + (static_cast<int64_t>(sp.t0) + kC * c) * a.o_tok + h * a.dv + r;
-        for (int t = 0; t < n; ++t) op[t * a.o_tok] = tile[t * 128];
-      }
-      __syncwarp();
-    }
-    if (warp == kOutWarp && lane == 0) bulk_wait_read<0>();  // the tile stays until the last store has read it
+    if (OUT && (warp & 3) == 0 && lane == 0) bulk_wait_read<0>();  // the tiles stay until the last store has read them
     __syncwarp();
-    }
   } else {
     // ----------------------------------------------------------- control ---
     const int grp = h / static_cast<int>(a.H / a.G);
@@ -997,22 +998,23 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const uint64_t kd = umma_desc_k_sw128(stage);
       const uint64_t td = panel_desc(stage + M::kImg);
       wait(full(c), (c >> 1) & 1, 40);
-      // Y = S K^T, least terms first
+      // Y = S K^T, least terms first, a half's 32 key channels at a time: what is left after the last is short
 #pragma unroll
-      for (int b = 0; b < KA; ++b) {
-        wait(bar(kSReady0 + b), ph, 41);
+      for (int st = 0; st < 2 * KA; ++st) {
+        wait(bar(kSReady0 + st), ph, 41);
         tcgen05_fence_after();
         if (elect_one()) {
+          const int hf = st / KA, b = st % KA;
 #pragma unroll
           for (int t = 2; t >= 0; --t)
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int k = w * QC + 16 * b;  // key channels k .. k + 15
-              umma_f16_ts(tmem + kTmY, tmem + kTmS + (w >> 1) * 96 + t * (HC / 2) + (w & 1) * (QC / 2) + 8 * b,
+            for (int w = 0; w < 2; ++w) {
+              const int k = hf * HC + w * QC + 16 * b;  // key channels k .. k + 15
+              umma_f16_ts(tmem + kTmY, tmem + kTmS + hf * 96 + t * (HC / 2) + w * (QC / 2) + 8 * b,
                           desc_add(kd, (k / 64) * 2 * kAtom + (k % 64) * 2), chunk_idesc(64, false),
-                          !(b == 0 && t == 2 && w == 0));
+                          !(st == 0 && t == 2 && w == 0));
             }
-          if (b == KA - 1) umma_commit(bar(kYDone));
+          if (st == 2 * KA - 1) umma_commit(bar(kYDone));
         }
         __syncwarp();
       }
@@ -1262,16 +1264,16 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st) {
   ChunkMaps m;
   const bool packed = a.cu != nullptr;
   auto map4 = [&](CUtensorMap* out, const void* base, int64_t n, int64_t heads, int64_t tok, int64_t seq,
-                  uint32_t box, CUtensorMapSwizzle swz) {
+                  uint32_t box, uint32_t tokens, CUtensorMapSwizzle swz) {
     const uint64_t dims[4] = {uint64_t(n), uint64_t(heads), uint64_t(a.L), packed ? 1 : uint64_t(a.batch)};
     const uint64_t strides[3] = {uint64_t(n * 2), uint64_t(tok * 2), uint64_t(seq * 2)};
-    const uint32_t b[4] = {box, 1, kC, 1};
+    const uint32_t b[4] = {box, 1, tokens, 1};
     return encode_map(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, b, swz);
   };
-  if (!map4(&m.q, a.q, a.dk, a.G, a.q_tok, a.q_seq, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map4(&m.k, a.k, a.dk, a.G, a.k_tok, a.k_seq, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map4(&m.v, a.v, a.dv, a.H, a.v_tok, a.v_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !map4(&m.out, a.out, a.dv, a.H, a.o_tok, a.o_seq, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
+  if (!map4(&m.q, a.q, a.dk, a.G, a.q_tok, a.q_seq, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map4(&m.k, a.k, a.dk, a.G, a.k_tok, a.k_seq, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !map4(&m.v, a.v, a.dv, a.H, a.v_tok, a.v_seq, 128, kC, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !map4(&m.out, a.out, a.dv, a.H, a.o_tok, a.o_seq, 128, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const ChunkPlan p = chunk_plan(a.batch, a.L, a.H, a.dk, a.dv, packed);
   return a.dk > 64 ? launch_chunk<2>(m, a, p, ws, st) : launch_chunk<1>(m, a, p, ws, st);
