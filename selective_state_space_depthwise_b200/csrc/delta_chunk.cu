@@ -219,8 +219,8 @@ struct ChunkMaps {
 };
 
 // ------------------------------------------------------------------- prep ---
-// One CTA of 4 warps per chunk and up to kPrepHeads heads of one key group,
-// four to an SM. Thread pt owns row pt of the 128 x 64 product [K; Q] K^T (one
+// One CTA of 4 warps per chunk and up to kPrepHeads heads of one key group.
+// Thread pt owns row pt of the 128 x 64 product [K; Q] K^T (one
 // set of MMAs per CTA; tensor memory keeps it for all its heads): rows 0-63
 // give A, rows 64-127 the scores.
 //
@@ -237,9 +237,10 @@ constexpr int kALd = 68;  // floats between rows of A (16-byte rows, conflict-fr
 
 template <int KA>  // 64-column atoms of d_key
 struct PrepSmem {
-  // from 0, per atom: K, then Q
-  static constexpr int kA = KA * 2 * kAtom;
-  static constexpr int kVec = kA + kC * kALd * 4;     // per head: Ghi, Glo, beta [64]
+  // from 0, per atom: K, then Q; A in their place once their product and norms are formed
+  static constexpr int kA = 0;
+  static constexpr int kAEnd = kC * kALd * 4;
+  static constexpr int kVec = KA * 2 * kAtom > kAEnd ? KA * 2 * kAtom : kAEnd;  // per head: Ghi, Glo, beta [64]
   static constexpr int kRk = kVec + kPrepHeads * 3 * kC * 4;  // 1 / |k| [64]
   static constexpr int kCf = kRk + kC * 4;            // column factors [3][64]
   static constexpr int kBar = kCf + 3 * kC * 4;
@@ -297,7 +298,7 @@ __device__ __forceinline__ void block_store(float* D, int lane, const float (&c)
 }
 
 template <int KA>
-__global__ void __launch_bounds__(128, 4)
+__global__ void __launch_bounds__(128, 6)
     delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int head_sets) {
   using M = PrepSmem<KA>;
   extern __shared__ unsigned char smem_raw[];
@@ -1113,43 +1114,66 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 }
 
 // First states of segments 2 .. count - 1: S_{p+1} = S_p M_p + H_p, H_p lying
-// where S_{p+1} goes. One block per 16 rows of a (sequence, head) through all
-// segments, a thread per key channel; fp32 throughout.
-constexpr int kJoinRows = 16;
+// where S_{p+1} goes. One block per 32 rows of a (sequence, head) through all
+// segments, M_{p+1} on its way to shared memory while M_p is used (read from L2
+// inside the product instead, a step takes 16 us, not 4). A warp has 8 rows, a
+// lane 4 key channels of them; fp32 throughout.
+constexpr int kJoinRows = 32, kJoinLd = 132;
+constexpr int kJoinSmem = (2 * 128 * 128 + kJoinRows * kJoinLd) * 4;
 __global__ void __launch_bounds__(128) delta_join_kernel(const DeltaArgs a, const Segments sg, int row_blocks) {
-  __shared__ float4 St[128][kJoinRows / 4];  // S_p transposed: [key channel][row]
+  extern __shared__ __align__(16) float join_smem[];
+  float* Ss = join_smem + 2 * 128 * 128;  // S_p [row][key channel]
   const int64_t sh = blockIdx.x / row_blocks;
-  const int r0 = static_cast<int>(blockIdx.x % row_blocks) * kJoinRows, col = threadIdx.x;
-  const int dk = static_cast<int>(a.dk), nr = min(kJoinRows, static_cast<int>(a.dv) - r0);
+  const int dk = static_cast<int>(a.dk), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = static_cast<int>(blockIdx.x % row_blocks) * kJoinRows + 8 * warp, col = 4 * lane;
+  const int nr = min(8, static_cast<int>(a.dv) - r0);  // rows of this warp, none or fewer behind the last
+  const bool in = col < dk;
   const int64_t one = a.dv * a.dk;
-  float* S = sg.S + sh * sg.count * one + static_cast<int64_t>(r0) * dk;
+  float* S = sg.S + sh * sg.count * one + static_cast<int64_t>(r0) * dk + col;
   const float* Mp = sg.M + sh * (sg.count - 2) * dk * dk;
-  float acc[kJoinRows];
+  auto fetch = [&](int p) {  // M_p, p >= 1
+    if (p + 1 < sg.count) {
+      const uint32_t dst = smem_u32(join_smem + (p & 1) * 128 * 128);
+      const float* src = Mp + static_cast<int64_t>(p - 1) * dk * dk;
+      for (int i = threadIdx.x; i < dk * dk / 4; i += 128) cp_async_16(dst + 16 * i, src + 4 * i);
+    }
+    cp_async_commit();
+  };
+  auto load = [&](int p, float4 (&v)[8]) {  // S_p's or H_{p-1}'s part of this thread
 #pragma unroll
-  for (int r = 0; r < kJoinRows; ++r) acc[r] = r < nr && col < dk ? S[one + r * dk + col] : 0.0f;
-  for (int p = 1; p + 1 < sg.count; ++p, Mp += dk * dk) {
+    for (int r = 0; r < 8; ++r)
+      v[r] = r < nr && in ? *reinterpret_cast<const float4*>(S + p * one + r * dk) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  fetch(1);
+  float4 acc[8];
+  load(1, acc);
+  for (int p = 1; p + 1 < sg.count; ++p) {
+    fetch(p + 1);
+    float* mine = Ss + 8 * warp * kJoinLd;  // a warp reads its own rows only
+#pragma unroll
+    for (int r = 0; r < 8; ++r) *reinterpret_cast<float4*>(mine + r * kJoinLd + col) = acc[r];
+    load(p + 1, acc);
+    cp_async_wait<1>();
     __syncthreads();
+    const float* Ms = join_smem + (p & 1) * 128 * 128 + (in ? col : 0);
+#pragma unroll 2
+    for (int k = 0; k < dk; k += 4) {
+      float4 m[4];
 #pragma unroll
-    for (int r = 0; r < kJoinRows; r += 4) St[col][r / 4] = make_float4(acc[r], acc[r + 1], acc[r + 2], acc[r + 3]);
-    __syncthreads();
-    float* next = S + (p + 1) * one;
+      for (int z = 0; z < 4; ++z) m[z] = *reinterpret_cast<const float4*>(Ms + (k + z) * dk);
 #pragma unroll
-    for (int r = 0; r < kJoinRows; ++r) acc[r] = r < nr && col < dk ? next[r * dk + col] : 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < dk; ++k) {
-      const float m = col < dk ? Mp[k * dk + col] : 0.0f;
-#pragma unroll
-      for (int r = 0; r < kJoinRows; r += 4) {
-        const float4 v = St[k][r / 4];
-        acc[r] = fmaf(v.x, m, acc[r]);
-        acc[r + 1] = fmaf(v.y, m, acc[r + 1]);
-        acc[r + 2] = fmaf(v.z, m, acc[r + 2]);
-        acc[r + 3] = fmaf(v.w, m, acc[r + 3]);
+      for (int r = 0; r < 8; ++r) {
+        const float4 w = *reinterpret_cast<const float4*>(mine + r * kJoinLd + k);
+        acc[r].x = fmaf(w.x, m[0].x, fmaf(w.y, m[1].x, fmaf(w.z, m[2].x, fmaf(w.w, m[3].x, acc[r].x))));
+        acc[r].y = fmaf(w.x, m[0].y, fmaf(w.y, m[1].y, fmaf(w.z, m[2].y, fmaf(w.w, m[3].y, acc[r].y))));
+        acc[r].z = fmaf(w.x, m[0].z, fmaf(w.y, m[1].z, fmaf(w.z, m[2].z, fmaf(w.w, m[3].z, acc[r].z))));
+        acc[r].w = fmaf(w.x, m[0].w, fmaf(w.y, m[1].w, fmaf(w.z, m[2].w, fmaf(w.w, m[3].w, acc[r].w))));
       }
     }
 #pragma unroll
-    for (int r = 0; r < kJoinRows; ++r)
-      if (r < nr && col < dk) next[r * dk + col] = acc[r];
+    for (int r = 0; r < 8; ++r)
+      if (r < nr && in) *reinterpret_cast<float4*>(S + (p + 1) * one + r * dk) = acc[r];
+    __syncthreads();  // M_p's buffer and the rows are free
   }
 }
 
@@ -1233,6 +1257,7 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
     err = cudaFuncSetAttribute(prep, kAttr, prep_smem);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true>, kAttr, smem);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_join_kernel, kAttr, kJoinSmem);
     if (err != cudaSuccess) return err;
     if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
@@ -1248,7 +1273,7 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   if (err != cudaSuccess) return err;
   if (p.count > 2) {
     const int rb = static_cast<int>((a.dv + kJoinRows - 1) / kJoinRows);
-    delta_join_kernel<<<static_cast<unsigned>(bh * rb), 128, 0, st>>>(a, sg, rb);
+    delta_join_kernel<<<static_cast<unsigned>(bh * rb), 128, kJoinSmem, st>>>(a, sg, rb);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
   return launch_chain<KA, true>(maps, a, img, p, sg, units * p.count, false, st);
