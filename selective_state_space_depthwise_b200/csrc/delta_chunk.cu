@@ -299,7 +299,8 @@ __device__ __forceinline__ void block_store(float* D, int lane, const float (&c)
 
 template <int KA>
 __global__ void __launch_bounds__(128, 6)
-    delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int head_sets) {
+    delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int head_sets,
+                      uint32_t* next) {
   using M = PrepSmem<KA>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(128, 6)
     s = static_cast<int>(slot / nc), c = static_cast<int>(slot % nc);
   }
   const Span sp = span_of(a, s);
+  if (blockIdx.x == 0 && pt < 2) next[pt] = 0u;  // the walks handed out, pass 1 and 2
   griddep_launch_dependents();  // the walk may set up; it waits for this grid before it reads the workspace
   if (c < 0 || kC * c >= sp.len) return;
   const int n = min(kC, sp.len - kC * c), tok = sp.t0 + kC * c;
@@ -623,6 +625,95 @@ constexpr uint32_t kTmY = 320;    // Y, then U
 constexpr uint32_t kTmO = 384;    // Q S^T, then with the scores' product
 constexpr uint32_t kTmU = 448;    // U's two output terms
 
+// A long sequence with few heads leaves most SMs idle, so it may be walked in
+// segments at once. The state is linear in the one before it: S_{p+1} = S_p M_p
+// + H_p, H_p a segment's walk from zero and M_p its walk of the identity without
+// values. Pass 1 (states only, OUT = false) forms both for every segment that
+// needs them, segment 0 from the state given; delta_join_kernel folds them into
+// the segments' first states; pass 2 walks all segments. More than twice the
+// work of one walk, on more than twice the SMs.
+//
+// Sequences of one length are cut on the host (count segments of per chunks).
+// The lengths of packed ones are known on the device alone: with `cut`, every
+// block works out the same cut for itself (delta_cut).
+struct Segments {
+  int count, per;   // 1: one walk
+  int cut;          // packed: cut on the device
+  int items;        // walks of this launch, where the host knows them
+  float* S;         // [segment][head][d_value][d_key]: the segments' first states
+  float* M;         // [segment][head][d_key][d_key]
+  uint32_t* next;   // walks handed out beyond one per block: pass 1's, pass 2's
+  int sms;
+};
+
+constexpr int kCutSeqs = 256;  // most packed sequences that are cut
+constexpr int kCutLeast = 8;   // least chunks of a segment of theirs
+// Segments before sequence s (all; those pass 1 walks from a state; those it walks from the identity), and the chunks
+// of a segment.
+struct Cut {
+  int all[kCutSeqs + 1], walk[kCutSeqs + 1], ident[kCutSeqs + 1];
+  int chunks[kCutSeqs];
+  int per;
+};
+
+// Time of a packed batch in chunks, cut into segments of `per`: the longest walk or the work of all over the SMs,
+// whichever is more, for both passes; launches and the join as in choose_segments.
+__device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int slices, int sms) {
+  float w1 = 0.0f, w2 = 0.0f;
+  for (int s = 0; s < n; ++s) {
+    const int segs = (c.chunks[s] + per - 1) / per;
+    w2 += static_cast<float>(c.chunks[s] * slices);
+    if (segs > 1) w1 += static_cast<float>(((segs - 1) * slices + segs - 2) * per);
+  }
+  const float scale = static_cast<float>(heads) / static_cast<float>(sms), len = static_cast<float>(per);
+  const float second = fmaxf(len, w2 * scale + 0.5f * len) + 2.5f;
+  if (per >= longest) return second;
+  return 0.85f * fmaxf(len, w1 * scale + 0.5f * len) + second + 5.5f +
+         1.6f * static_cast<float>((longest + per - 1) / per - 2);
+}
+
+// All threads of a block; ends with a barrier.
+__device__ __forceinline__ void delta_cut(const DeltaArgs& a, int slices, int sms, Cut& c) {
+  const int n = static_cast<int>(a.batch), tid = threadIdx.x;
+  for (int s = tid; s < n; s += blockDim.x) c.chunks[s] = (span_of(a, s).len + kC - 1) / kC;
+  __syncthreads();
+  if (tid < 32) {  // lane l: the longest in l + 1 segments
+    int longest = 1;
+    for (int s = 0; s < n; ++s) longest = max(longest, c.chunks[s]);
+    const int per = (longest + tid) / (tid + 1);
+    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), slices, sms);
+    if (tid > 0) cost = per < kCutLeast ? 3.0e38f : cost * 1.05f;
+    int best = tid;
+    for (int m = 16; m > 0; m >>= 1) {
+      const float oc = __shfl_xor_sync(0xffffffffu, cost, m);
+      const int ob = __shfl_xor_sync(0xffffffffu, best, m);
+      if (oc < cost || (oc == cost && ob < best)) cost = oc, best = ob;
+    }
+    if (tid == 0) c.per = (longest + best) / (best + 1);
+  }
+  __syncthreads();
+  if (tid < 3) {
+    int* out = tid == 0 ? c.all : tid == 1 ? c.walk : c.ident;
+    int sum = 0;
+    for (int s = 0; s < n; ++s) {
+      out[s] = sum;
+      sum += max(max(1, (c.chunks[s] + c.per - 1) / c.per) - tid, 0);
+    }
+    out[n] = sum;
+  }
+  __syncthreads();
+}
+// The sequence that item i of a running sum belongs to.
+__device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (sums[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 template <int KA>
 struct ChainSmem {
   static constexpr int kKQ = KA * 2 * kAtom;  // per atom: K, then Q
@@ -631,8 +722,9 @@ struct ChainSmem {
   static constexpr int kStage = (kImg + kImgStride + 1023) / 1024 * 1024;
   static constexpr int kOut = kStages * kStage;      // two chunks of [token][128] bf16
   static constexpr int kBad = kOut + 2 * kC * 256;   // int [4][128]
-  static constexpr int kBar = kBad + 4 * 128 * 4;
-  static constexpr int kMisc = kBar + (kStages + 16) * 8;  // TMEM address, abort flag
+  static constexpr int kCut = kBad + 4 * 128 * 4;
+  static constexpr int kBar = kCut + (static_cast<int>(sizeof(Cut)) + 15) / 16 * 16;
+  static constexpr int kMisc = kBar + (kStages + 16) * 8;  // TMEM address, abort flag, next item
   static constexpr int kTotal = kMisc + 16;
   static_assert(kTotal + 1024 <= 232448, "227 KB of shared memory");
   static constexpr uint32_t kTx = static_cast<uint32_t>(kImg + kImgBytes);
@@ -643,21 +735,6 @@ enum Bar {  // after the stages' full barriers; each completes once a chunk
   kOaDone, kOFree, kNumNamed
 };
 static_assert(kNumNamed <= 15, "barrier count");
-
-// A long sequence with few heads leaves most SMs idle, so it may be walked in
-// `count` segments of `per` chunks at once. The state is linear in the one
-// before it: S_{p+1} = S_p M_p + H_p, H_p a segment's walk from zero and M_p
-// its walk of the identity without values. Pass 1 (states only, OUT = false)
-// forms both for every segment that needs them, segment 0 from the state given;
-// delta_join_kernel folds them into the segments' first states; pass 2 walks
-// all segments. More than twice the work of one walk, on more than twice the SMs.
-struct Segments {
-  int count, per;  // count 1: one walk
-  float* S;        // [sequence, head][count][d_value][d_key]: the segments' first states
-  float* M;        // [sequence, head][count - 2][d_key][d_key]: M_1 ..
-};
-
-constexpr int kOrderSeqs = 256;  // packed sequences up to which the walk starts with the longest
 
 template <int KA, bool OUT>
 __global__ void __launch_bounds__(kChainThreads, 1)
@@ -673,45 +750,6 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31;
   const Shifter sh{a.two16};
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  // This block's sequence, head, rows and segment; `ident`: it walks the identity.
-  const int H = static_cast<int>(a.H);
-  int unit = static_cast<int>(blockIdx.x), seg = 0;
-  bool ident = false;
-  if constexpr (OUT) {
-    seg = unit % sg.count, unit /= sg.count;
-  } else {
-    const int walks = static_cast<int>(a.batch) * H * slices * (sg.count - 1);
-    ident = unit >= walks;
-    if (ident) {
-      unit -= walks;
-      seg = 1 + unit % (sg.count - 2), unit = unit / (sg.count - 2) * slices;
-    } else {
-      seg = unit % (sg.count - 1), unit /= sg.count - 1;
-    }
-  }
-  const int slice = unit % slices, seq_head = unit / slices, h = seq_head % H;
-  int s = seq_head / H;
-  if (a.cu && a.batch <= kOrderSeqs) {  // sequence of rank s by length, the longest first
-    int* lens = reinterpret_cast<int*>(smem + M::kBad);
-    const int nseq = static_cast<int>(a.batch);
-    if (tid < nseq) lens[tid] = span_of(a, tid).len;
-    __syncthreads();
-    if (tid < nseq) {
-      int rank = 0;
-      for (int i = 0; i < nseq; ++i) rank += lens[i] > lens[tid] || (lens[i] == lens[tid] && i < tid);
-      if (rank == s) lens[kOrderSeqs] = tid;
-    }
-    __syncthreads();
-    s = lens[kOrderSeqs];
-  }
-  Span sp = span_of(a, s);
-  const int64_t slot0 = slot_of(a, s, sp.t0) + static_cast<int64_t>(seg) * sg.per;
-  if (sg.count > 1) {
-    sp.t0 += kC * sg.per * seg;
-    sp.len = max(0, min(sp.len - kC * sg.per * seg, kC * sg.per));
-  }
-  const int nc = (sp.len + kC - 1) / kC;
-
   auto bar = [&](int b) { return sb + M::kBar + 8 * (kStages + b); };
   auto full = [&](int c) { return sb + M::kBar + 8 * (c & 1); };
   volatile int* abort = reinterpret_cast<volatile int*>(smem + M::kMisc + 4);
@@ -740,6 +778,45 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
   const uint32_t tm = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);  // this warp's lane quarter
   const int row = 32 * (warp & 3) + lane;
+  const int H = static_cast<int>(a.H), nseq = static_cast<int>(a.batch);
+  Cut& cut = *reinterpret_cast<Cut*>(smem + M::kCut);
+  if (sg.cut) delta_cut(a, slices, sg.sms, cut);
+  const int walks = sg.cut ? cut.walk[nseq] * H * slices : nseq * H * slices * (sg.count - 1);
+  const int items = !sg.cut ? sg.items : OUT ? cut.all[nseq] * H * slices : walks + cut.ident[nseq] * H;
+  griddep_wait();  // the prep's tiles, and the counter of walks
+  // Walks until none is left. `done`: chunks of the walks before this one, so that the barriers' phases run on.
+  int done = 0;
+  for (int item = static_cast<int>(blockIdx.x); item < items;) {
+  // This walk's sequence, head, rows and segment; `ident`: of the identity.
+  const bool ident = !OUT && item >= walks;
+  int slice, h, s, seg = 0, count = sg.count, first_seg = 0;  // first_seg: the sequence's first segment
+  {
+    int i = ident ? item - walks : item;
+    const int sl = ident ? 1 : slices;
+    if (sg.cut) {
+      slice = i % sl, i /= sl;
+      h = i % H, i /= H;
+      const int* sums = ident ? cut.ident : OUT ? cut.all : cut.walk;
+      s = cut_find(sums, nseq, i);
+      seg = i - sums[s] + (ident ? 1 : 0);
+      count = cut.all[s + 1] - cut.all[s];
+      first_seg = cut.all[s];
+    } else {
+      const int segs = OUT ? count : ident ? count - 2 : count - 1;
+      seg = i % segs + (ident ? 1 : 0), i /= segs;
+      slice = i % sl, i /= sl;
+      h = i % H, s = i / H;
+      first_seg = s * count;
+    }
+  }
+  const int per = sg.cut ? cut.per : sg.per;
+  Span sp = span_of(a, s);
+  const int64_t slot0 = slot_of(a, s, sp.t0) + static_cast<int64_t>(seg) * per;
+  if (count > 1) {
+    sp.t0 += kC * per * seg;
+    sp.len = max(0, min(sp.len - kC * per * seg, kC * per));
+  }
+  const int nc = (sp.len + kC - 1) / kC;
   const int r = slice * 128 + row, rows = static_cast<int>(ident ? a.dk : a.dv);
   const bool row_in = r < rows;
   auto arrive = [&](int b) {
@@ -755,10 +832,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const int64_t at = static_cast<int64_t>(row_in ? r : 0) * a.dk + quarter * QC;  // this thread's part of a state
     const int64_t shi = static_cast<int64_t>(s) * H + h, one = a.dv * a.dk;
     const float* from = a.state_in ? a.state_in + shi * one : nullptr;
-    if (sg.count > 1) {
+    float* seg_state = sg.S + (static_cast<int64_t>(first_seg + seg) * H + h) * one;
+    if (count > 1) {
       if (OUT) {
-        griddep_wait();  // the joined states
-        if (seg > 0 || a.state_in) from = sg.S + (shi * sg.count + seg) * one;
+        if (seg > 0 || a.state_in) from = seg_state;
       } else if (seg > 0) {
         from = nullptr;
       }
@@ -769,7 +846,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (from && row_in && i < cols) v = *reinterpret_cast<const float4*>(from + at + i);
       if (!OUT && from && row_in && i < cols)  // state_out may be state_in: pass 2 reads a copy
-        *reinterpret_cast<float4*>(sg.S + shi * sg.count * one + at + i) = v;
+        *reinterpret_cast<float4*>(seg_state + at + i) = v;
       if (!OUT && ident) {
         const int d = r - quarter * QC - i;
         v = make_float4(d == 0, d == 1, d == 2, d == 3);
@@ -790,7 +867,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     auto store_chunk = [&](int c) {
       const int n = min(kC, sp.len - kC * c), t0 = 16 * quarter;
       __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem + M::kOut + (c & 1) * kC * 256) + t0 * 128 + row;
-      wait(bar(kOaDone), c & 1, 39);
+      wait(bar(kOaDone), (done + c) & 1, 39);
       tcgen05_fence_after();
       uint32_t d[16];
       tmem_ld_x16(tm + kTmO + t0, d);
@@ -826,7 +903,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const uint32_t tm_y = tm + kTmY + 16 * quarter;                          // its 16 tokens
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
-      const uint32_t ph = c & 1;
+      const int g = done + c;
+      const uint32_t ph = g & 1;
       unsigned char* stage = smem + ph * M::kStage;
       const Coef& cf = *reinterpret_cast<const Coef*>(stage + M::kImg + kImgCoef);
       const int n = min(kC, sp.len - kC * c);
@@ -837,7 +915,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       if (a.cu && n < kC) {
         // Keys behind the sequence (the next packed one's) meet zeros of U: they must be finite.
-        wait(full(c), (c >> 1) & 1, 34);
+        wait(full(g), (g >> 1) & 1, 34);
         for (int e = tid; e < KA * kC * 8; e += 32 * kStateWarps) {
           const int t = e / (kC * 8), i = e / 8 % kC;
           if (i >= n) *reinterpret_cast<uint4*>(stage + t * 2 * kAtom + i * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -856,7 +934,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       }
       if (OUT && c > 0) store_chunk(c - 1);
       // R = V - e^G Y
-      wait(full(c), (c >> 1) & 1, 34);
+      wait(full(g), (g >> 1) & 1, 34);
       decay = cf.decay;
       const unsigned char* vt = stage + M::kV + row * 2 + 16 * quarter * 256;
       // V, read while the product runs, and what must stay out of R: `marks`, tokens that are not finite, and `drop`,
@@ -949,14 +1027,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     }
     if (nc > 0) {
       if constexpr (OUT) store_chunk(nc - 1);
-      wait(bar(kSDone0 + half), (nc - 1) & 1, 33);
+      wait(bar(kSDone0 + half), (done + nc - 1) & 1, 33);
       tcgen05_fence_after();
 #pragma unroll
       for (int i0 = 0; i0 < QC; i0 += 16) update(i0);
     }
     float* to = a.state_out + shi * one;
-    if (!OUT) to = ident ? sg.M + (shi * (sg.count - 2) + seg - 1) * a.dk * a.dk : sg.S + (shi * sg.count + seg + 1) * one;
-    if (row_in && (!OUT || seg == sg.count - 1)) {
+    if (!OUT) to = ident ? sg.M + (static_cast<int64_t>(first_seg + seg) * H + h) * a.dk * a.dk : seg_state + H * one;
+    if (row_in && (!OUT || seg == count - 1)) {
 #pragma unroll
       for (int i = 0; i < QC; i += 4)
         if (i < cols) {
@@ -978,27 +1056,28 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       loaded = c + 1;
       if (elect_one()) {
         const int tok = sp.t0 + kC * c;
-        const uint32_t base = sb + (c & 1) * M::kStage;
-        mbar_arrive_expect_tx(full(c), M::kTx);
+        const int g = done + c;
+        const uint32_t base = sb + (g & 1) * M::kStage;
+        mbar_arrive_expect_tx(full(g), M::kTx);
 #pragma unroll
         for (int t = 0; t < KA; ++t) {
-          tma_load_4d(base + t * 2 * kAtom, &maps.k, 64 * t, grp, tok, sp.seq, full(c));
-          tma_load_4d(base + t * 2 * kAtom + kAtom, &maps.q, 64 * t, grp, tok, sp.seq, full(c));
+          tma_load_4d(base + t * 2 * kAtom, &maps.k, 64 * t, grp, tok, sp.seq, full(g));
+          tma_load_4d(base + t * 2 * kAtom + kAtom, &maps.q, 64 * t, grp, tok, sp.seq, full(g));
         }
-        tma_load_4d(base + M::kV, &maps.v, 128 * slice, h, tok, sp.seq, full(c));
-        bulk_load(base + M::kImg, img + static_cast<int64_t>(c) * a.H * kImgStride, kImgBytes, full(c));
+        tma_load_4d(base + M::kV, &maps.v, 128 * slice, h, tok, sp.seq, full(g));
+        bulk_load(base + M::kImg, img + static_cast<int64_t>(c) * a.H * kImgStride, kImgBytes, full(g));
       }
       __syncwarp();
     };
-    griddep_wait();  // the prep's workspace
     for (int c = 0; c < min(nc, kStages); ++c) load(c);
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
-      const uint32_t ph = c & 1;
+      const int g = done + c;
+      const uint32_t ph = g & 1;
       const uint32_t stage = sb + ph * M::kStage;
       const uint64_t kd = umma_desc_k_sw128(stage);
       const uint64_t td = panel_desc(stage + M::kImg);
-      wait(full(c), (c >> 1) & 1, 40);
+      wait(full(g), (g >> 1) & 1, 40);
       // Y = S K^T, least terms first, a half's 32 key channels at a time: what is left after the last is short
 #pragma unroll
       for (int st = 0; st < 2 * KA; ++st) {
@@ -1096,21 +1175,28 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     if (*abort) {
       for (int c = max(0, loaded - kStages); c < loaded; ++c) {
         const uint64_t w0 = globaltimer_ns();
-        while (!mbar_try_wait(full(c), (c >> 1) & 1) && globaltimer_ns() - w0 < 2000000000ull) {
+        while (!mbar_try_wait(full(done + c), ((done + c) >> 1) & 1) && globaltimer_ns() - w0 < 2000000000ull) {
         }
       }
       spin_ns(1000000);  // products take microseconds
     } else if (nc > 0) {
-      wait(bar(OUT ? kOaDone : kSDone1), (nc - 1) & 1, 39);
+      wait(bar(OUT ? kOaDone : kSDone1), (done + nc - 1) & 1, 39);
     }
   }
   __syncwarp();
   tcgen05_fence_before();
-  __syncthreads();
-  if (warp == kCtlWarp) {
-    tcgen05_fence_after();
-    tmem_dealloc(tmem, 512);
+  if (tid == 0) {
+    int next = items;
+    if (items > static_cast<int>(gridDim.x)) next = static_cast<int>(gridDim.x + atomicAdd(sg.next + (OUT ? 1 : 0), 1u));
+    *reinterpret_cast<volatile int*>(smem + M::kMisc + 8) = next;
   }
+  __syncthreads();
+  tcgen05_fence_after();
+  item = *reinterpret_cast<volatile int*>(smem + M::kMisc + 8);
+  done += nc;
+  __syncthreads();
+  }
+  if (warp == kCtlWarp) tmem_dealloc(tmem, 512);
 }
 
 // First states of segments 2 .. count - 1: S_{p+1} = S_p M_p + H_p, H_p lying
@@ -1119,22 +1205,30 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 // inside the product instead, a step takes 16 us, not 4). A warp has 8 rows, a
 // lane 4 key channels of them; fp32 throughout.
 constexpr int kJoinRows = 32, kJoinLd = 132;
-constexpr int kJoinSmem = (2 * 128 * 128 + kJoinRows * kJoinLd) * 4;
-__global__ void __launch_bounds__(128) delta_join_kernel(const DeltaArgs a, const Segments sg, int row_blocks) {
+constexpr int kJoinSmem = (2 * 128 * 128 + kJoinRows * kJoinLd) * 4 + static_cast<int>(sizeof(Cut));
+__global__ void __launch_bounds__(128)
+    delta_join_kernel(const DeltaArgs a, const Segments sg, int slices, int row_blocks) {
   extern __shared__ __align__(16) float join_smem[];
   float* Ss = join_smem + 2 * 128 * 128;  // S_p [row][key channel]
-  const int64_t sh = blockIdx.x / row_blocks;
+  const int H = static_cast<int>(a.H), sh = static_cast<int>(blockIdx.x) / row_blocks, s = sh / H;
+  int count = sg.count, first_seg = s * count;
+  if (sg.cut) {
+    Cut& cut = *reinterpret_cast<Cut*>(Ss + kJoinRows * kJoinLd);
+    delta_cut(a, slices, sg.sms, cut);
+    first_seg = cut.all[s], count = cut.all[s + 1] - first_seg;
+  }
+  if (count < 3) return;
   const int dk = static_cast<int>(a.dk), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = static_cast<int>(blockIdx.x % row_blocks) * kJoinRows + 8 * warp, col = 4 * lane;
   const int nr = min(8, static_cast<int>(a.dv) - r0);  // rows of this warp, none or fewer behind the last
   const bool in = col < dk;
-  const int64_t one = a.dv * a.dk;
-  float* S = sg.S + sh * sg.count * one + static_cast<int64_t>(r0) * dk + col;
-  const float* Mp = sg.M + sh * (sg.count - 2) * dk * dk;
+  const int64_t index = static_cast<int64_t>(first_seg) * H + sh % H, step = a.dv * a.dk * H;
+  float* S = sg.S + index * a.dv * a.dk + static_cast<int64_t>(r0) * dk + col;
+  const float* Mp = sg.M + index * dk * dk;
   auto fetch = [&](int p) {  // M_p, p >= 1
-    if (p + 1 < sg.count) {
+    if (p + 1 < count) {
       const uint32_t dst = smem_u32(join_smem + (p & 1) * 128 * 128);
-      const float* src = Mp + static_cast<int64_t>(p - 1) * dk * dk;
+      const float* src = Mp + static_cast<int64_t>(p) * H * dk * dk;
       for (int i = threadIdx.x; i < dk * dk / 4; i += 128) cp_async_16(dst + 16 * i, src + 4 * i);
     }
     cp_async_commit();
@@ -1142,12 +1236,12 @@ __global__ void __launch_bounds__(128) delta_join_kernel(const DeltaArgs a, cons
   auto load = [&](int p, float4 (&v)[8]) {  // S_p's or H_{p-1}'s part of this thread
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-      v[r] = r < nr && in ? *reinterpret_cast<const float4*>(S + p * one + r * dk) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[r] = r < nr && in ? *reinterpret_cast<const float4*>(S + p * step + r * dk) : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   fetch(1);
   float4 acc[8];
   load(1, acc);
-  for (int p = 1; p + 1 < sg.count; ++p) {
+  for (int p = 1; p + 1 < count; ++p) {
     fetch(p + 1);
     float* mine = Ss + 8 * warp * kJoinLd;  // a warp reads its own rows only
 #pragma unroll
@@ -1172,7 +1266,7 @@ __global__ void __launch_bounds__(128) delta_join_kernel(const DeltaArgs a, cons
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r)
-      if (r < nr && in) *reinterpret_cast<float4*>(S + (p + 1) * one + r * dk) = acc[r];
+      if (r < nr && in) *reinterpret_cast<float4*>(S + (p + 1) * step + r * dk) = acc[r];
     __syncthreads();  // M_p's buffer and the rows are free
   }
 }
@@ -1182,21 +1276,21 @@ int64_t chunk_slots(int64_t batch, int64_t L, bool packed) {
 }
 
 // Segments of a walk of nc chunks with `units` (sequence, head, slice) on
-// `sms` SMs, in units of a chunk's time (3.4 us): one walk takes nc for each
-// wave of units; pass 1 walks at 0.9, and the extra launches and the join cost
-// about 8 chunks and half a chunk a segment. Lengths of packed sequences are
-// known on the device alone: one walk each.
-int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int sms, int* per) {
+// `sms` SMs, in units of a chunk's time (3.4 us): a wave of walks takes its
+// chunks (0.85 of them in pass 1) and 2.5 to start, the extra launches 3, the
+// join 1.6 a segment and wave of its blocks. (Times of 1 to 32 segments for 2 to
+// 60 heads and 2048 to 32768 tokens: the choice is within 10% of the best.)
+int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int64_t dv, int sms, int* per) {
   auto waves = [sms](int64_t blocks) { return static_cast<double>((blocks + sms - 1) / sms); };
-  const double single = static_cast<double>(nc) * waves(units);
-  double best = 0.85 * single;
+  double best = 0.95 * (static_cast<double>(nc) + 2.5) * waves(units);
   int count = 1;
   *per = static_cast<int>(nc);
   for (int64_t p = 2; p <= 64 && 4 * p <= nc && units * p <= 64 * sms; ++p) {
     const int64_t len = (nc + p - 1) / p;
     if ((nc + len - 1) / len != p) continue;
-    const double cost = static_cast<double>(len) * (0.9 * waves(units * (p - 1) + seq_heads * (p - 2)) + waves(units * p)) +
-                        8.0 + 0.5 * static_cast<double>(p);
+    const double w1 = waves(units * (p - 1) + seq_heads * (p - 2)), w2 = waves(units * p);
+    const double cost = static_cast<double>(len) * (0.85 * w1 + w2) + 2.5 * (w1 + w2) + 3.0 +
+                        1.6 * static_cast<double>(p - 2) * waves(seq_heads * ((dv + kJoinRows - 1) / kJoinRows));
     if (cost < best) best = cost, count = static_cast<int>(p), *per = static_cast<int>(len);
   }
   return count;
@@ -1204,36 +1298,46 @@ int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int sms, int* 
 
 struct ChunkPlan {
   int64_t slots;
-  int slices, count, per;
-  size_t S, M, bytes;  // offsets of the segments' states behind the operand tiles, and the end
+  int slices, count, per, sms;
+  bool cut;
+  size_t next, S, M, bytes;  // offsets behind the operand tiles, and the end
 };
 ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv, bool packed) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  else cudaGetLastError();  // no device: the default SM count
+  int dev = 0;
   ChunkPlan p{};
+  p.sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || p.sms <= 0) {
+    cudaGetLastError();  // no device: the default SM count
+    p.sms = 148;
+  }
   p.slots = chunk_slots(batch, L, packed);
   p.slices = static_cast<int>((dv + 127) / 128);
   const int64_t nc = (L + kC - 1) / kC;
-  p.count = packed ? 1 : choose_segments(nc, batch * H * p.slices, batch * H, sms > 0 ? sms : 148, &p.per);
+  p.count = 1, p.per = static_cast<int>(nc);
+  if (packed)  // some sequence may be long enough to cut
+    p.cut = batch <= kCutSeqs && nc >= 4 * kCutLeast && (nc + batch) * H * p.slices < (1 << 28);
+  else
+    p.count = choose_segments(nc, batch * H * p.slices, batch * H, dv, p.sms, &p.per);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  p.S = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
-  p.M = p.bytes = p.S;
-  if (p.count > 1) {
-    p.M = up(p.S + static_cast<size_t>(batch * H * p.count * dv * dk) * 4);
-    p.bytes = up(p.M + static_cast<size_t>(batch * H * (p.count - 2) * dk * dk) * 4);
+  p.next = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
+  p.S = p.M = p.bytes = p.next + 256;
+  if (p.count > 1 || p.cut) {
+    const int64_t segs = p.cut ? p.slots / kCutLeast + batch : batch * p.count;
+    p.M = up(p.S + static_cast<size_t>(segs * H * dv * dk) * 4);
+    p.bytes = up(p.M + static_cast<size_t>(segs * H * dk * dk) * 4);
   }
   return p;
 }
 
 template <int KA, bool OUT>
 cudaError_t launch_chain(const ChunkMaps& maps, const DeltaArgs& a, const unsigned char* img, const ChunkPlan& p,
-                         const Segments& sg, int64_t blocks, bool after_prep, cudaStream_t st) {
+                         const Segments& sg, bool after_prep, cudaStream_t st) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>(sg.cut || sg.items > p.sms ? p.sms : sg.items));
   cfg.blockDim = dim3(kChainThreads);
   cfg.dynamicSmemBytes = ChainSmem<KA>::kTotal + 1024;
   cfg.stream = st;
@@ -1262,21 +1366,23 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
     if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
   const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
-  prep<<<static_cast<unsigned>(p.slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets);
+  const int64_t bh = a.batch * a.H, units = bh * p.slices;
+  Segments sg{p.count, p.per, p.cut, static_cast<int>(units * p.count), reinterpret_cast<float*>(img + p.S),
+              reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), p.sms};
+  prep<<<static_cast<unsigned>(p.slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets, sg.next);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  const int64_t bh = a.batch * a.H, units = bh * p.slices;
-  Segments sg{p.count, p.per, nullptr, nullptr};
-  if (p.count == 1) return launch_chain<KA, true>(maps, a, img, p, sg, units, true, st);
-  sg.S = reinterpret_cast<float*>(img + p.S), sg.M = reinterpret_cast<float*>(img + p.M);
-  err = launch_chain<KA, false>(maps, a, img, p, sg, units * (p.count - 1) + bh * (p.count - 2), true, st);
+  if (p.count == 1 && !p.cut) return launch_chain<KA, true>(maps, a, img, p, sg, true, st);
+  Segments first = sg;
+  first.items = static_cast<int>(units * (p.count - 1) + bh * (p.count - 2));
+  err = launch_chain<KA, false>(maps, a, img, p, first, true, st);
   if (err != cudaSuccess) return err;
-  if (p.count > 2) {
+  if (p.count > 2 || p.cut) {
     const int rb = static_cast<int>((a.dv + kJoinRows - 1) / kJoinRows);
-    delta_join_kernel<<<static_cast<unsigned>(bh * rb), 128, kJoinSmem, st>>>(a, sg, rb);
+    delta_join_kernel<<<static_cast<unsigned>(bh * rb), 128, kJoinSmem, st>>>(a, sg, p.slices, rb);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
-  return launch_chain<KA, true>(maps, a, img, p, sg, units * p.count, false, st);
+  return launch_chain<KA, true>(maps, a, img, p, sg, false, st);
 }
 
 }  // namespace
