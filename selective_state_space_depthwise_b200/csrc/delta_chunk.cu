@@ -648,11 +648,12 @@ struct Segments {
 
 constexpr int kCutSeqs = 256;  // most packed sequences that are cut
 constexpr int kCutLeast = 8;   // least chunks of a segment of theirs
-// Segments before sequence s (all; those pass 1 walks from a state; those it walks from the identity), and the chunks
-// of a segment.
+// Sequences in the order of their lengths, the longest first, so that the last walks handed out are short. For each
+// place: the sequence, and the segments before it (all; those pass 1 walks from a state; those it walks from the
+// identity). `per`: chunks of a segment.
 struct Cut {
   int all[kCutSeqs + 1], walk[kCutSeqs + 1], ident[kCutSeqs + 1];
-  int chunks[kCutSeqs];
+  int chunks[kCutSeqs], seq[kCutSeqs];
   int per;
 };
 
@@ -666,20 +667,25 @@ __device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int long
     if (segs > 1) w1 += static_cast<float>(((segs - 1) * slices + segs - 2) * per);
   }
   const float scale = static_cast<float>(heads) / static_cast<float>(sms), len = static_cast<float>(per);
-  const float second = fmaxf(len, w2 * scale + 0.5f * len) + 2.5f;
+  const float second = fmaxf(len, w2 * scale + 0.3f * len) + 2.5f;
   if (per >= longest) return second;
-  return 0.85f * fmaxf(len, w1 * scale + 0.5f * len) + second + 5.5f +
+  return 0.85f * fmaxf(len, w1 * scale + 0.3f * len) + second + 5.5f +
          1.6f * static_cast<float>((longest + per - 1) / per - 2);
 }
 
 // All threads of a block; ends with a barrier.
 __device__ __forceinline__ void delta_cut(const DeltaArgs& a, int slices, int sms, Cut& c) {
   const int n = static_cast<int>(a.batch), tid = threadIdx.x;
-  for (int s = tid; s < n; s += blockDim.x) c.chunks[s] = (span_of(a, s).len + kC - 1) / kC;
+  for (int s = tid; s < n; s += blockDim.x) c.all[s] = (span_of(a, s).len + kC - 1) / kC;
+  __syncthreads();
+  for (int s = tid; s < n; s += blockDim.x) {
+    int place = 0;
+    for (int i = 0; i < n; ++i) place += c.all[i] > c.all[s] || (c.all[i] == c.all[s] && i < s);
+    c.chunks[place] = c.all[s], c.seq[place] = s;
+  }
   __syncthreads();
   if (tid < 32) {  // lane l: the longest in l + 1 segments
-    int longest = 1;
-    for (int s = 0; s < n; ++s) longest = max(longest, c.chunks[s]);
+    const int longest = max(1, c.chunks[0]);
     const int per = (longest + tid) / (tid + 1);
     float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), slices, sms);
     if (tid > 0) cost = per < kCutLeast ? 3.0e38f : cost * 1.05f;
@@ -703,7 +709,7 @@ __device__ __forceinline__ void delta_cut(const DeltaArgs& a, int slices, int sm
   }
   __syncthreads();
 }
-// The sequence that item i of a running sum belongs to.
+// The place that item i of a running sum belongs to.
 __device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
@@ -797,10 +803,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       slice = i % sl, i /= sl;
       h = i % H, i /= H;
       const int* sums = ident ? cut.ident : OUT ? cut.all : cut.walk;
-      s = cut_find(sums, nseq, i);
-      seg = i - sums[s] + (ident ? 1 : 0);
-      count = cut.all[s + 1] - cut.all[s];
-      first_seg = cut.all[s];
+      const int place = cut_find(sums, nseq, i);
+      s = cut.seq[place];
+      seg = i - sums[place] + (ident ? 1 : 0);
+      count = cut.all[place + 1] - cut.all[place];
+      first_seg = cut.all[place];
     } else {
       const int segs = OUT ? count : ident ? count - 2 : count - 1;
       seg = i % segs + (ident ? 1 : 0), i /= segs;
@@ -1210,16 +1217,16 @@ __global__ void __launch_bounds__(128)
     delta_join_kernel(const DeltaArgs a, const Segments sg, int slices, int row_blocks) {
   extern __shared__ __align__(16) float join_smem[];
   float* Ss = join_smem + 2 * 128 * 128;  // S_p [row][key channel]
-  const int H = static_cast<int>(a.H), sh = static_cast<int>(blockIdx.x) / row_blocks, s = sh / H;
+  const int H = static_cast<int>(a.H);
+  Cut& cut = *reinterpret_cast<Cut*>(Ss + kJoinRows * kJoinLd);
+  if (sg.cut) delta_cut(a, slices, sg.sms, cut);
+  for (int item = static_cast<int>(blockIdx.x); item < static_cast<int>(a.batch) * H * row_blocks; item += gridDim.x) {
+  const int sh = item / row_blocks, s = sh / H;  // with a cut: the place in its order, the longest first
   int count = sg.count, first_seg = s * count;
-  if (sg.cut) {
-    Cut& cut = *reinterpret_cast<Cut*>(Ss + kJoinRows * kJoinLd);
-    delta_cut(a, slices, sg.sms, cut);
-    first_seg = cut.all[s], count = cut.all[s + 1] - first_seg;
-  }
-  if (count < 3) return;
+  if (sg.cut) first_seg = cut.all[s], count = cut.all[s + 1] - first_seg;
+  if (count < 3) break;
   const int dk = static_cast<int>(a.dk), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = static_cast<int>(blockIdx.x % row_blocks) * kJoinRows + 8 * warp, col = 4 * lane;
+  const int r0 = item % row_blocks * kJoinRows + 8 * warp, col = 4 * lane;
   const int nr = min(8, static_cast<int>(a.dv) - r0);  // rows of this warp, none or fewer behind the last
   const bool in = col < dk;
   const int64_t index = static_cast<int64_t>(first_seg) * H + sh % H, step = a.dv * a.dk * H;
@@ -1268,6 +1275,7 @@ __global__ void __launch_bounds__(128)
     for (int r = 0; r < 8; ++r)
       if (r < nr && in) *reinterpret_cast<float4*>(S + (p + 1) * step + r * dk) = acc[r];
     __syncthreads();  // M_p's buffer and the rows are free
+  }
   }
 }
 
@@ -1379,7 +1387,8 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   if (err != cudaSuccess) return err;
   if (p.count > 2 || p.cut) {
     const int rb = static_cast<int>((a.dv + kJoinRows - 1) / kJoinRows);
-    delta_join_kernel<<<static_cast<unsigned>(bh * rb), 128, kJoinSmem, st>>>(a, sg, p.slices, rb);
+    const int64_t blocks = bh * rb < p.sms ? bh * rb : p.sms;  // one an SM
+    delta_join_kernel<<<static_cast<unsigned>(blocks), 128, kJoinSmem, st>>>(a, sg, p.slices, rb);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
   return launch_chain<KA, true>(maps, a, img, p, sg, false, st);
