@@ -244,7 +244,7 @@ struct PrepSmem {
   static constexpr int kRk = kVec + kPrepHeads * 3 * kC * 4;  // 1 / |k| [64]
   static constexpr int kCf = kRk + kC * 4;            // column factors [3][64]
   static constexpr int kBar = kCf + 3 * kC * 4;
-  static constexpr int kTotal = kBar + 32;  // full, done, TMEM address, abort flag
+  static constexpr int kTotal = kBar + 32;  // full, done, TMEM address, abort flag, tokens not finite
 };
 
 // A fp32 value as two tf32 ones: 11 bits, and the rest (13 bits, of which the product reads 11).
@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(128, 6)
   float* As = reinterpret_cast<float*>(smem + M::kA);
   float* rk = reinterpret_cast<float*>(smem + M::kRk);
   float* cfac = reinterpret_cast<float*>(smem + M::kCf);
+  uint32_t* bad_tokens = reinterpret_cast<uint32_t*>(smem + M::kBar + 24);
   const int h0 = grp * rep + set * kPrepHeads, nh = min(kPrepHeads, rep - set * kPrepHeads);
   // Warp w: head h0 + w. Running sums of g in log2 units and fp64, kept as two
   // floats, so that differences of far sums stay exact; a decay below 2^-256 is 0 anyway.
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(128, 6)
       if (i == kC - 1) cf->decay = eg;
       const bool bad = i < n && (k_bad || !(fabsf(Gi) <= 3.4028235e38f) || !(fabsf(beta[i]) <= 3.4028235e38f));
       const uint32_t bits = __ballot_sync(0xffffffffu, bad);
-      if (lane == 0) cf->bad[warp] = bits;
+      if (lane == 0) cf->bad[warp] = bits, bad_tokens[warp] = bits;
     }
     {  // column factors of block row b, columns j < 16 b
       const int b = pt < 48 ? 3 : pt < 96 ? 2 : 1, j = pt < 48 ? pt : pt < 96 ? pt - 64 : pt - 96;
@@ -460,6 +461,8 @@ __global__ void __launch_bounds__(128, 6)
       }
     }
     __syncthreads();
+    // Tokens that are not finite stay out of A: their rows and columns would spread to tokens before them.
+    const uint64_t bad_mask = bad_tokens[0] | static_cast<uint64_t>(bad_tokens[1]) << 32;
     const float lead = is_q ? rn * a.scale : rn * beta[i];
     const float rfac = bi > 0 ? lead * ex2_approx((Gi - Ghi[16 * bi - 1]) + (Gl - Glo[16 * bi - 1])) : 0.0f;
     // 8 values of this row from column j on: to A, or to the scores
@@ -467,6 +470,11 @@ __global__ void __launch_bounds__(128, 6)
       if (n < kC && !is_q && i >= n) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+      }
+      if (bad_mask && !is_q) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if ((bad_mask >> i | bad_mask >> (j + e)) & 1) f[e] = 0.0f;
       }
       if (mine) {
         if (is_q) {

@@ -223,6 +223,95 @@ def test_long_sequences():
         check(*api.delta_prefill(**x, state_in=s0), *rule(**x, state=s0), f"{b} x {L}")
 
 
+@pytest.mark.parametrize("decay", [0.02, 1.0])
+@pytest.mark.parametrize("b,L,G,H,dk,dv", [(1, 3000, 2, 2, 128, 128), (1, 9001, 1, 1, 96, 40), (2, 2111, 1, 3, 64, 192),
+                                           (1, 4097, 4, 16, 128, 128)])
+def test_long_sequences_of_few_heads(b, L, G, H, dk, dv, decay):
+    """Walked in segments that are joined: decays weak enough that the first state reaches the last segment, and
+    state_out over state_in."""
+    x = inputs((b, L), G, H, dk, dv, seed=L, decay=decay, l2norm=True)
+    s0 = state0(b, H, dv, dk, L)
+    want = rule(**x, state=s0, l2norm=True)
+    check(*api.delta_prefill(**x, state_in=s0, qk_l2norm=True), *want)
+    out, st = api.delta_prefill(**x, state_in=s0, state_out=s0, qk_l2norm=True)
+    check(out, st, *want)
+    assert st.data_ptr() == s0.data_ptr()
+
+
+@pytest.mark.parametrize("lens,G,H,dk,dv", [
+    ([5000], 1, 2, 128, 128), ([3000, 0, 1, 700, 64], 2, 4, 64, 72), ([130, 4097, 63, 2000], 1, 3, 128, 192),
+    ([1] * 40 + [3333] + [70] * 9, 2, 8, 128, 128), ([9] * 299 + [2500], 1, 2, 64, 64), ([0] * 20 + [2100], 1, 1, 128, 8),
+])
+def test_long_packed_sequences(lens, G, H, dk, dv):
+    """Long packed sequences, cut into segments on the device, next to short and empty ones; more sequences than are
+    cut."""
+    T, n = sum(lens), len(lens)
+    x = inputs((1, T), G, H, dk, dv, seed=T, decay=0.05)
+    s0 = state0(n, H, dv, dk, T)
+    at = torch.tensor([0] + lens).cumsum(0)
+    out, st = api.delta_prefill(**{m: t[0] for m, t in x.items()}, state_in=s0, cu_seqlens=at.int().cuda())
+    # the sequences of one length together
+    for m in sorted(set(lens)):
+        which = [i for i in range(n) if lens[i] == m]
+        rows = torch.stack([torch.arange(at[i], at[i] + m) for i in which]).cuda()
+        want = rule(**{k: t[0][rows] for k, t in x.items()}, state=s0[which])
+        check(out[rows], st[which], *want, f"length {m}")
+
+
+@pytest.mark.parametrize("L", [17, 130, 2500])
+@pytest.mark.parametrize("what", ["k", "g", "beta", "v"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_values_that_are_not_finite_stay_behind_their_token(L, what, value):
+    """A key, decay, beta or value that is not finite at one token: outputs before it are those of the shorter
+    sequence, none from it on is finite (of v: in its row and head), and so is the state."""
+    t, H, dv = 2 * L // 3, 2, 64
+    x = inputs((1, L), 1, H, 128, dv, seed=L, decay=0.1)
+    want, _ = rule(**{n: y[:, :t] for n, y in x.items()})
+    bad = {n: y.clone() for n, y in x.items()}
+    if what == "k":
+        bad["k"][0, t, 0, 5] = value
+    elif what == "v":
+        bad["v"][0, t, 1, 7] = value
+    else:
+        bad[what][0, t] = value
+    out, st = api.delta_prefill(**bad)
+    check(out[:, :t], torch.zeros(1), want, torch.zeros(1))
+    if what == "v":
+        assert not torch.isfinite(out[0, t:, 1, 7]).any() and not torch.isfinite(st[0, 1, 7]).any()
+        keep = torch.ones(H, dv, dtype=torch.bool)
+        keep[1, 7] = False
+        full, wst = rule(**x)
+        check(out[:, :, keep], st[:, keep], full[:, :, keep], wst[:, keep])
+    else:
+        assert not torch.isfinite(out[0, t:]).any() and not torch.isfinite(st).any()
+
+
+@pytest.mark.parametrize("L", [17, 130, 2500])
+def test_a_query_that_is_not_finite_stays_at_its_token(L):
+    t = 2 * L // 3
+    x = inputs((1, L), 1, 2, 128, 64, seed=L)
+    want, wst = rule(**x)
+    x["q"][0, t, 0, 3] = float("nan")
+    out, st = api.delta_prefill(**x)
+    keep = [i for i in range(L) if i != t]
+    check(out[:, keep], st, want[:, keep], wst)
+    assert out[0, t].isnan().all()
+
+
+@pytest.mark.parametrize("L", [17, 200, 2500])
+def test_a_state_that_is_not_finite_stays_in_its_row(L):
+    x = inputs((1, L), 1, 2, 64, 64, seed=L)
+    s0 = state0(1, 2, 64, 64, L)
+    s0[0, 1, 9, 3] = float("nan")
+    out, st = api.delta_prefill(**x, state_in=s0)
+    s0[0, 1, 9, 3] = 0
+    want, wst = rule(**x, state=s0)
+    keep = torch.ones(2, 64, dtype=torch.bool)
+    keep[1, 9] = False
+    check(out[:, :, keep], st[:, keep], want[:, :, keep], wst[:, keep])
+    assert not torch.isfinite(out[0, :, 1, 9]).any() and not torch.isfinite(st[0, 1, 9]).any()
+
+
 def test_many_units():
     """More (sequence, head) units than SMs, two slices of d_value."""
     x = inputs((5, 140), 8, 32, 64, 256, seed=43)
