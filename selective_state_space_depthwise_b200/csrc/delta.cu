@@ -254,7 +254,7 @@ extern "C" {
 
 size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims* dims, int32_t packed) {
   if (ssm::delta_shape(dims, true) != SSM_OK || !ssm::takes_chunks(dims->seqlen, packed)) return 0;
-  return ssm::delta_chunk_workspace(dims->batch, dims->seqlen, dims->nheads, dims->d_key, dims->d_value, packed);
+  return ssm::delta_chunk_workspace(dims->batch, dims->seqlen, dims->nheads, dims->ngroups, dims->d_key, dims->d_value, packed);
 }
 
 ssm_status ssm_delta_prefill(const ssm_delta_dims* dims, const void* q, const void* k, const void* v, const float* g,
@@ -269,7 +269,7 @@ ssm_status ssm_delta_prefill(const ssm_delta_dims* dims, const void* q, const vo
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t err;
   if (ssm::takes_chunks(a.L, a.cu)) {
-    const size_t need = ssm::delta_chunk_workspace(a.batch, a.L, a.H, a.dk, a.dv, a.cu);
+    const size_t need = ssm::delta_chunk_workspace(a.batch, a.L, a.H, a.G, a.dk, a.dv, a.cu);
     if (!workspace || !ssm::aligned(workspace, 256))
       return fail(SSM_ERR_INVALID_ARG, "workspace is NULL or not 256-byte aligned");
     if (workspace_bytes < need)

@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(128, 6)
       const double o = __shfl_up_sync(0xffffffffu, sum, d);
       if (lane >= d) sum += o;
     }
-    const double first = sum - g1;
+    const double before = __shfl_up_sync(0xffffffffu, sum, 1);
+    const double first = (lane ? before : 0.0) + g0;  // not sum - g1: g1 may not be finite
     const float f0 = static_cast<float>(first), f1 = static_cast<float>(sum);
     *reinterpret_cast<float2*>(vec + 2 * lane) = make_float2(f0, f1);
     *reinterpret_cast<float2*>(vec + kC + 2 * lane) =
@@ -651,6 +652,7 @@ struct Segments {
   float* S;         // [segment][head][d_value][d_key]: the segments' first states
   float* M;         // [segment][head][d_key][d_key]
   uint32_t* next;   // walks handed out beyond one per block: pass 1's, pass 2's
+  int walkers;      // walks of one segment of a sequence: its heads times the slices of d_value, or pairs of heads
   int sms;
 };
 
@@ -667,14 +669,14 @@ struct Cut {
 
 // Time of a packed batch in chunks, cut into segments of `per`: the longest walk or the work of all over the SMs,
 // whichever is more, for both passes; launches and the join as in choose_segments.
-__device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int slices, int sms) {
+__device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int walkers, int sms) {
   float w1 = 0.0f, w2 = 0.0f;
   for (int s = 0; s < n; ++s) {
     const int segs = (c.chunks[s] + per - 1) / per;
-    w2 += static_cast<float>(c.chunks[s] * slices);
-    if (segs > 1) w1 += static_cast<float>(((segs - 1) * slices + segs - 2) * per);
+    w2 += static_cast<float>(c.chunks[s] * walkers);
+    if (segs > 1) w1 += static_cast<float>(((segs - 1) * walkers + (segs - 2) * heads) * per);
   }
-  const float scale = static_cast<float>(heads) / static_cast<float>(sms), len = static_cast<float>(per);
+  const float scale = 1.0f / static_cast<float>(sms), len = static_cast<float>(per);
   const float second = fmaxf(len, w2 * scale + 0.3f * len) + 2.5f;
   if (per >= longest) return second;
   return 0.85f * fmaxf(len, w1 * scale + 0.3f * len) + second + 5.5f +
@@ -682,7 +684,7 @@ __device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int long
 }
 
 // All threads of a block; ends with a barrier.
-__device__ __forceinline__ void delta_cut(const DeltaArgs& a, int slices, int sms, Cut& c) {
+__device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int sms, Cut& c) {
   const int n = static_cast<int>(a.batch), tid = threadIdx.x;
   for (int s = tid; s < n; s += blockDim.x) c.all[s] = (span_of(a, s).len + kC - 1) / kC;
   __syncthreads();
@@ -695,7 +697,7 @@ __device__ __forceinline__ void delta_cut(const DeltaArgs& a, int slices, int sm
   if (tid < 32) {  // lane l: the longest in l + 1 segments
     const int longest = max(1, c.chunks[0]);
     const int per = (longest + tid) / (tid + 1);
-    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), slices, sms);
+    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms);
     if (tid > 0) cost = per < kCutLeast ? 3.0e38f : cost * 1.05f;
     int best = tid;
     for (int m = 16; m > 0; m >>= 1) {
@@ -728,20 +730,22 @@ __device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
   return lo;
 }
 
-template <int KA>
+template <int KA, bool PAIR>
 struct ChainSmem {
+  static constexpr int kImgs = PAIR ? 2 : 1;  // heads
+  static constexpr int kOuts = PAIR ? 1 : 2;  // output tiles
   static constexpr int kKQ = KA * 2 * kAtom;  // per atom: K, then Q
   static constexpr int kV = kKQ;              // [token][128]
   static constexpr int kImg = kV + kC * 256;
-  static constexpr int kStage = (kImg + kImgStride + 1023) / 1024 * 1024;
-  static constexpr int kOut = kStages * kStage;      // two chunks of [token][128] bf16
-  static constexpr int kBad = kOut + 2 * kC * 256;   // int [4][128]
+  static constexpr int kStage = (kImg + kImgs * kImgStride + 1023) / 1024 * 1024;
+  static constexpr int kOut = kStages * kStage;          // [token][128] bf16, kOuts chunks
+  static constexpr int kBad = kOut + kOuts * kC * 256;   // int [4][128]
   static constexpr int kCut = kBad + 4 * 128 * 4;
   static constexpr int kBar = kCut + (static_cast<int>(sizeof(Cut)) + 15) / 16 * 16;
   static constexpr int kMisc = kBar + (kStages + 16) * 8;  // TMEM address, abort flag, next item
   static constexpr int kTotal = kMisc + 16;
   static_assert(kTotal + 1024 <= 232448, "227 KB of shared memory");
-  static constexpr uint32_t kTx = static_cast<uint32_t>(kImg + kImgBytes);
+  static constexpr uint32_t kTx = static_cast<uint32_t>(kImg + kImgs * kImgBytes);
 };
 
 enum Bar {  // after the stages' full barriers; each completes once a chunk
@@ -750,11 +754,11 @@ enum Bar {  // after the stages' full barriers; each completes once a chunk
 };
 static_assert(kNumNamed <= 15, "barrier count");
 
-template <int KA, bool OUT>
+template <int KA, bool OUT, bool PAIR>
 __global__ void __launch_bounds__(kChainThreads, 1)
     delta_chain_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, const unsigned char* img0,
                        int slices, const Segments sg) {
-  using M = ChainSmem<KA>;
+  using M = ChainSmem<KA, PAIR>;
   constexpr int DK = 64 * KA;
   constexpr int HC = DK / 2;  // key channels of a half: of two state warpgroups
   constexpr int QC = DK / 4;  // key channels of a state thread: KA steps of 16
@@ -794,9 +798,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int row = 32 * (warp & 3) + lane;
   const int H = static_cast<int>(a.H), nseq = static_cast<int>(a.batch);
   Cut& cut = *reinterpret_cast<Cut*>(smem + M::kCut);
-  if (sg.cut) delta_cut(a, slices, sg.sms, cut);
-  const int walks = sg.cut ? cut.walk[nseq] * H * slices : nseq * H * slices * (sg.count - 1);
-  const int items = !sg.cut ? sg.items : OUT ? cut.all[nseq] * H * slices : walks + cut.ident[nseq] * H;
+  if (sg.cut) delta_cut(a, sg.walkers, sg.sms, cut);
+  const int walks = sg.cut ? cut.walk[nseq] * sg.walkers : nseq * sg.walkers * (sg.count - 1);
+  const int items = !sg.cut ? sg.items : OUT ? cut.all[nseq] * sg.walkers : walks + cut.ident[nseq] * H;
   griddep_wait();  // the prep's tiles, and the counter of walks
   // Walks until none is left. `done`: chunks of the walks before this one, so that the barriers' phases run on.
   int done = 0;
@@ -806,10 +810,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   int slice, h, s, seg = 0, count = sg.count, first_seg = 0;  // first_seg: the sequence's first segment
   {
     int i = ident ? item - walks : item;
-    const int sl = ident ? 1 : slices;
+    const int sl = ident ? 1 : slices, heads = PAIR && !ident ? H / 2 : H;
     if (sg.cut) {
       slice = i % sl, i /= sl;
-      h = i % H, i /= H;
+      h = i % heads, i /= heads;
       const int* sums = ident ? cut.ident : OUT ? cut.all : cut.walk;
       const int place = cut_find(sums, nseq, i);
       s = cut.seq[place];
@@ -820,7 +824,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const int segs = OUT ? count : ident ? count - 2 : count - 1;
       seg = i % segs + (ident ? 1 : 0), i /= segs;
       slice = i % sl, i /= sl;
-      h = i % H, s = i / H;
+      h = i % heads, s = i / heads;
       first_seg = s * count;
     }
   }
@@ -832,7 +836,10 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     sp.len = max(0, min(sp.len - kC * per * seg, kC * per));
   }
   const int nc = (sp.len + kC - 1) / kC;
-  const int r = slice * 128 + row, rows = static_cast<int>(ident ? a.dk : a.dv);
+  // With PAIR, h is a pair of heads: rows 0-63 head 2 h, rows 64-127 head 2 h + 1. The identity is one head's.
+  const int head0 = PAIR && !ident ? 2 * h : h, head1 = PAIR && !ident ? 2 * h + 1 : h;
+  const int mine = PAIR ? (warp & 3) >> 1 : 0;  // which of the two this warp's rows are of
+  const int r = slice * 128 + row, rows = static_cast<int>(ident ? a.dk : PAIR ? 128 : a.dv);
   const bool row_in = r < rows;
   auto arrive = [&](int b) {
     tcgen05_fence_before();
@@ -845,9 +852,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     const int quarter = warp >> 2, half = quarter >> 1;
     const int cols = static_cast<int>(min(static_cast<int64_t>(QC), max(a.dk - quarter * QC, static_cast<int64_t>(0))));
     const int64_t at = static_cast<int64_t>(row_in ? r : 0) * a.dk + quarter * QC;  // this thread's part of a state
-    const int64_t shi = static_cast<int64_t>(s) * H + h, one = a.dv * a.dk;
+    const int64_t shi = static_cast<int64_t>(s) * H + head0, one = a.dv * a.dk;  // a pair's states adjoin
     const float* from = a.state_in ? a.state_in + shi * one : nullptr;
-    float* seg_state = sg.S + (static_cast<int64_t>(first_seg + seg) * H + h) * one;
+    float* seg_state = sg.S + (static_cast<int64_t>(first_seg + seg) * H + head0) * one;
     if (count > 1) {
       if (OUT) {
         if (seg > 0 || a.state_in) from = seg_state;
@@ -881,7 +888,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     // Rounds and stores this thread's 16 tokens of chunk c, once the scores' product is in.
     auto store_chunk = [&](int c) {
       const int n = min(kC, sp.len - kC * c), t0 = 16 * quarter;
-      __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem + M::kOut + (c & 1) * kC * 256) + t0 * 128 + row;
+      __nv_bfloat16* tile = reinterpret_cast<__nv_bfloat16*>(smem + M::kOut + (c & 1) % M::kOuts * kC * 256) + t0 * 128 + row;
       wait(bar(kOaDone), (done + c) & 1, 39);
       tcgen05_fence_after();
       uint32_t d[16];
@@ -894,34 +901,39 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         for (int i = 0; i < 16; ++i)
           if (i >= first) d[i] = 0x7fffffffu;
       }
+      const bool issuer = (warp & 3) == 0 && lane == 0;
+      if constexpr (M::kOuts == 1) {  // the last chunk's store has read the tile
+        if (issuer) bulk_wait_read<0>();
+        named_bar_sync(1 + quarter, 128);
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) tile[i * 128] = __float2bfloat16_rn(__uint_as_float(d[i]));
       // A tile store per 16 tokens; it leaves out channels past d_value and tokens past L. The last tokens of a
       // packed sequence may end inside one: those rows are written one by one.
-      const bool issuer = (warp & 3) == 0 && lane == 0;
       if (!a.cu || n >= t0 + 16) {
         fence_proxy_async_smem();
         if (issuer) bulk_wait_read<0>();  // the last chunk's store has read its half of the tiles
         named_bar_sync(1 + quarter, 128);
         if (issuer) {
-          tma_store_4d(&maps.out, sb + M::kOut + (c & 1) * kC * 256 + t0 * 256, 128 * slice, h, sp.t0 + kC * c + t0,
+          tma_store_4d(&maps.out, sb + M::kOut + (c & 1) % M::kOuts * kC * 256 + t0 * 256, 128 * slice, h, sp.t0 + kC * c + t0,
                        sp.seq);
           bulk_commit();
         }
       } else if (row_in) {
-        __nv_bfloat16* op = a.out + (static_cast<int64_t>(sp.t0) + kC * c + t0) * a.o_tok + h * a.dv + r;
+        __nv_bfloat16* op = a.out + (static_cast<int64_t>(sp.t0) + kC * c + t0) * a.o_tok + head0 * a.dv + r;
         for (int t = 0; t0 + t < n; ++t) op[t * a.o_tok] = tile[t * 128];
       }
       __syncwarp();
     };
     const uint32_t tm_s = tm + kTmS + half * 96 + (quarter & 1) * (QC / 2);  // its columns of S's terms
     const uint32_t tm_y = tm + kTmY + 16 * quarter;                          // its 16 tokens
+    const uint32_t tm_u = PAIR && mine ? tm + kTmS + 16 * quarter : tm_y;    // of U
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       const int g = done + c;
       const uint32_t ph = g & 1;
       unsigned char* stage = smem + ph * M::kStage;
-      const Coef& cf = *reinterpret_cast<const Coef*>(stage + M::kImg + kImgCoef);
+      const Coef& cf = *reinterpret_cast<const Coef*>(stage + M::kImg + mine * kImgStride + kImgCoef);
       const int n = min(kC, sp.len - kC * c);
       // S as the A operand of Y and Q S^T
       if (c > 0) {
@@ -1012,7 +1024,7 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       uint64_t x[8], y[8];
       {
         uint32_t d[16];
-        tmem_ld_x16(tm_y, d);
+        tmem_ld_x16(tm_u, d);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = pk2u(d[2 * i], d[2 * i + 1]);
@@ -1034,8 +1046,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         uint32_t hi[8], mi[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2(sh, x[i], hi[i], mi[i]);
-        tmem_st_x8(tm + kTmU + 8 * quarter, hi);
-        tmem_st_x8(tm + kTmU + 32 + 8 * quarter, mi);
+        // A thread's 16 columns: eight of each term. Of a pair, each head's rows are zero in the other's operand.
+        const uint32_t other = tm + (mine ? kTmU : kTmY) + 16 * quarter;
+        tmem_st_x8(tm + (PAIR && mine ? kTmY : kTmU) + 16 * quarter, hi);
+        tmem_st_x8(tm + (PAIR && mine ? kTmY : kTmU) + 16 * quarter + 8, mi);
+        if constexpr (PAIR) {
+          const uint32_t zero[16] = {};
+          tmem_st_x16(other, zero);
+        }
         tmem_st_wait();
         arrive(kUoReady);
       }
@@ -1063,8 +1081,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
     __syncwarp();
   } else {
     // ----------------------------------------------------------- control ---
-    const int grp = h / static_cast<int>(a.H / a.G);
-    const unsigned char* img = img0 + (slot0 * a.H + h) * kImgStride;
+    const int grp = head0 / static_cast<int>(a.H / a.G);
+    const unsigned char* img = img0 + (slot0 * a.H + head0) * kImgStride;
     int loaded = 0;
     auto load = [&](int c) {
       if (*abort) return;
@@ -1081,6 +1099,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         tma_load_4d(base + M::kV, &maps.v, 128 * slice, h, tok, sp.seq, full(g));
         bulk_load(base + M::kImg, img + static_cast<int64_t>(c) * a.H * kImgStride, kImgBytes, full(g));
+        if constexpr (PAIR)
+          bulk_load(base + M::kImg + kImgStride,
+                    img + (static_cast<int64_t>(c) * a.H + head1 - head0) * kImgStride, kImgBytes, full(g));
       }
       __syncwarp();
     };
@@ -1093,6 +1114,8 @@ __global__ void __launch_bounds__(kChainThreads, 1)
       const uint64_t kd = umma_desc_k_sw128(stage);
       const uint64_t td = panel_desc(stage + M::kImg);
       wait(full(g), (g >> 1) & 1, 40);
+      // a pair's second scores' product reads an operand where Y goes
+      if (PAIR && OUT && c > 0) wait(bar(kOaDone), ph ^ 1u, 47);
       // Y = S K^T, least terms first, a half's 32 key channels at a time: what is left after the last is short
 #pragma unroll
       for (int st = 0; st < 2 * KA; ++st) {
@@ -1134,18 +1157,22 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         }
         __syncwarp();
       }
-      // U = R T^T: 16 tokens j at a time meet the tokens i from theirs on
+      // U = R T^T: 16 tokens j at a time meet the tokens i from theirs on. Of a pair, each head's T meets all rows,
+      // and its own rows are read of the result (the second where S's first terms were).
       wait(bar(kRReady), ph, 43);
+      if (PAIR && OUT) wait(bar(kOiDone), ph, 38);
       tcgen05_fence_after();
       if (elect_one()) {
         constexpr int kTt[6] = {2, 0, 1, 1, 0, 0}, kTr[6] = {0, 2, 1, 0, 1, 0};  // terms of T and R, least first
 #pragma unroll
-        for (int pr = 0; pr < 6; ++pr)
+        for (int hd = 0; hd < M::kImgs; ++hd)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_f16_ts(tmem + kTmY + 16 * kk, tmem + kTmDelta + 32 * kTr[pr] + 8 * kk,
-                        desc_add(td, kTt[pr] * kPanelTerm + panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
-                        pr + kk > 0);
+          for (int pr = 0; pr < 6; ++pr)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_f16_ts(tmem + (hd ? kTmS : kTmY) + 16 * kk, tmem + kTmDelta + 32 * kTr[pr] + 8 * kk,
+                          desc_add(td, hd * kImgStride + kTt[pr] * kPanelTerm + panel_off(kk)),
+                          chunk_idesc(64 - 16 * kk, false), pr + kk > 0);
         umma_commit(bar(kUDone));
       }
       __syncwarp();
@@ -1174,12 +1201,14 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         if (elect_one()) {
           constexpr int kTp[3] = {1, 0, 0}, kTu[3] = {0, 1, 0};
 #pragma unroll
-          for (int pr = 0; pr < 3; ++pr)
+          for (int hd = 0; hd < M::kImgs; ++hd)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_f16_ts(tmem + kTmO + 16 * kk, tmem + kTmU + 32 * kTu[pr] + 8 * kk,
-                          desc_add(td, kImgP + kTp[pr] * kPanelTerm + panel_off(kk)), chunk_idesc(64 - 16 * kk, false),
-                          true);
+            for (int pr = 0; pr < 3; ++pr)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f16_ts(tmem + kTmO + 16 * kk, tmem + (hd ? kTmY : kTmU) + 16 * kk + 8 * kTu[pr],
+                            desc_add(td, hd * kImgStride + kImgP + kTp[pr] * kPanelTerm + panel_off(kk)),
+                            chunk_idesc(64 - 16 * kk, false), true);
           umma_commit(bar(kOaDone));
         }
         __syncwarp();
@@ -1222,12 +1251,12 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 constexpr int kJoinRows = 32, kJoinLd = 132;
 constexpr int kJoinSmem = (2 * 128 * 128 + kJoinRows * kJoinLd) * 4 + static_cast<int>(sizeof(Cut));
 __global__ void __launch_bounds__(128)
-    delta_join_kernel(const DeltaArgs a, const Segments sg, int slices, int row_blocks) {
+    delta_join_kernel(const DeltaArgs a, const Segments sg, int row_blocks) {
   extern __shared__ __align__(16) float join_smem[];
   float* Ss = join_smem + 2 * 128 * 128;  // S_p [row][key channel]
   const int H = static_cast<int>(a.H);
   Cut& cut = *reinterpret_cast<Cut*>(Ss + kJoinRows * kJoinLd);
-  if (sg.cut) delta_cut(a, slices, sg.sms, cut);
+  if (sg.cut) delta_cut(a, sg.walkers, sg.sms, cut);
   for (int item = static_cast<int>(blockIdx.x); item < static_cast<int>(a.batch) * H * row_blocks; item += gridDim.x) {
   const int sh = item / row_blocks, s = sh / H;  // with a cut: the place in its order, the longest first
   int count = sg.count, first_seg = s * count;
@@ -1314,11 +1343,11 @@ int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int64_t dv, in
 
 struct ChunkPlan {
   int64_t slots;
-  int slices, count, per, sms;
-  bool cut;
+  int slices, walkers, count, per, sms;
+  bool cut, pair;
   size_t next, S, M, bytes;  // offsets behind the operand tiles, and the end
 };
-ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv, bool packed) {
+ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed) {
   int dev = 0;
   ChunkPlan p{};
   p.sms = 148;
@@ -1329,12 +1358,15 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv
   }
   p.slots = chunk_slots(batch, L, packed);
   p.slices = static_cast<int>((dv + 127) / 128);
+  // Heads of 64 channels: two that share their keys fill the 128 rows of a walk.
+  p.pair = dv == 64 && H / G % 2 == 0;
+  p.walkers = p.pair ? static_cast<int>(H / 2) : static_cast<int>(H) * p.slices;
   const int64_t nc = (L + kC - 1) / kC;
   p.count = 1, p.per = static_cast<int>(nc);
   if (packed)  // some sequence may be long enough to cut
     p.cut = batch <= kCutSeqs && nc >= 4 * kCutLeast && (nc + batch) * H * p.slices < (1 << 28);
   else
-    p.count = choose_segments(nc, batch * H * p.slices, batch * H, dv, p.sms, &p.per);
+    p.count = choose_segments(nc, batch * p.walkers, batch * H, dv, p.sms, &p.per);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.next = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
   p.S = p.M = p.bytes = p.next + 256;
@@ -1346,7 +1378,7 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv
   return p;
 }
 
-template <int KA, bool OUT>
+template <int KA, bool OUT, bool PAIR>
 cudaError_t launch_chain(const ChunkMaps& maps, const DeltaArgs& a, const unsigned char* img, const ChunkPlan& p,
                          const Segments& sg, bool after_prep, cudaStream_t st) {
   cudaLaunchAttribute attr{};
@@ -1355,17 +1387,17 @@ cudaError_t launch_chain(const ChunkMaps& maps, const DeltaArgs& a, const unsign
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(sg.cut || sg.items > p.sms ? p.sms : sg.items));
   cfg.blockDim = dim3(kChainThreads);
-  cfg.dynamicSmemBytes = ChainSmem<KA>::kTotal + 1024;
+  cfg.dynamicSmemBytes = ChainSmem<KA, PAIR>::kTotal + 1024;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = after_prep ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, delta_chain_kernel<KA, OUT>, maps, a, img, p.slices, sg);
+  return cudaLaunchKernelEx(&cfg, delta_chain_kernel<KA, OUT, PAIR>, maps, a, img, p.slices, sg);
 }
 
-template <int KA>
+template <int KA, bool PAIR>
 cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkPlan& p, void* ws, cudaStream_t st) {
   unsigned char* img = static_cast<unsigned char*>(ws);
-  const int prep_smem = PrepSmem<KA>::kTotal + 1024, smem = ChainSmem<KA>::kTotal + 1024;
+  const int prep_smem = PrepSmem<KA>::kTotal + 1024, smem = ChainSmem<KA, PAIR>::kTotal + 1024;
   auto prep = delta_prep_kernel<KA>;
   // The kernels' shared-memory limits, once per device.
   static std::atomic<uint64_t> ready{0};
@@ -1375,37 +1407,37 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
     constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     err = cudaFuncSetAttribute(prep, kAttr, prep_smem);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true>, kAttr, smem);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true, PAIR>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false, PAIR>, kAttr, smem);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_join_kernel, kAttr, kJoinSmem);
     if (err != cudaSuccess) return err;
     if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
   const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
-  const int64_t bh = a.batch * a.H, units = bh * p.slices;
+  const int64_t bh = a.batch * a.H, units = a.batch * p.walkers;
   Segments sg{p.count, p.per, p.cut, static_cast<int>(units * p.count), reinterpret_cast<float*>(img + p.S),
-              reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), p.sms};
+              reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), p.walkers, p.sms};
   prep<<<static_cast<unsigned>(p.slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets, sg.next);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
-  if (p.count == 1 && !p.cut) return launch_chain<KA, true>(maps, a, img, p, sg, true, st);
+  if (p.count == 1 && !p.cut) return launch_chain<KA, true, PAIR>(maps, a, img, p, sg, true, st);
   Segments first = sg;
   first.items = static_cast<int>(units * (p.count - 1) + bh * (p.count - 2));
-  err = launch_chain<KA, false>(maps, a, img, p, first, true, st);
+  err = launch_chain<KA, false, PAIR>(maps, a, img, p, first, true, st);
   if (err != cudaSuccess) return err;
   if (p.count > 2 || p.cut) {
     const int rb = static_cast<int>((a.dv + kJoinRows - 1) / kJoinRows);
     const int64_t blocks = bh * rb < p.sms ? bh * rb : p.sms;  // one an SM
-    delta_join_kernel<<<static_cast<unsigned>(blocks), 128, kJoinSmem, st>>>(a, sg, p.slices, rb);
+    delta_join_kernel<<<static_cast<unsigned>(blocks), 128, kJoinSmem, st>>>(a, sg, rb);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
-  return launch_chain<KA, true>(maps, a, img, p, sg, false, st);
+  return launch_chain<KA, true, PAIR>(maps, a, img, p, sg, false, st);
 }
 
 }  // namespace
 
-size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv, bool packed) {
-  return chunk_plan(batch, L, H, dk, dv, packed).bytes;
+size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed) {
+  return chunk_plan(batch, L, H, G, dk, dv, packed).bytes;
 }
 
 cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st) {
@@ -1418,13 +1450,15 @@ cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st) {
     const uint32_t b[4] = {box, 1, tokens, 1};
     return encode_map(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, b, swz);
   };
+  const ChunkPlan p = chunk_plan(a.batch, a.L, a.H, a.G, a.dk, a.dv, packed);
+  const int64_t rows = p.pair ? 128 : a.dv, heads = p.pair ? a.H / 2 : a.H;  // of v and out as the walk takes them
   if (!map4(&m.q, a.q, a.dk, a.G, a.q_tok, a.q_seq, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !map4(&m.k, a.k, a.dk, a.G, a.k_tok, a.k_seq, 64, kC, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      !map4(&m.v, a.v, a.dv, a.H, a.v_tok, a.v_seq, 128, kC, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !map4(&m.out, a.out, a.dv, a.H, a.o_tok, a.o_seq, 128, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
+      !map4(&m.v, a.v, rows, heads, a.v_tok, a.v_seq, 128, kC, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !map4(&m.out, a.out, rows, heads, a.o_tok, a.o_seq, 128, 16, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  const ChunkPlan p = chunk_plan(a.batch, a.L, a.H, a.dk, a.dv, packed);
-  return a.dk > 64 ? launch_chunk<2>(m, a, p, ws, st) : launch_chunk<1>(m, a, p, ws, st);
+  if (p.pair) return a.dk > 64 ? launch_chunk<2, true>(m, a, p, ws, st) : launch_chunk<1, true>(m, a, p, ws, st);
+  return a.dk > 64 ? launch_chunk<2, false>(m, a, p, ws, st) : launch_chunk<1, false>(m, a, p, ws, st);
 }
 
 }  // namespace ssm

@@ -26,7 +26,7 @@ struct DeltaArgs {
 
 // 64 tokens at a time on the tensor cores; a.L > 0.
 cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st);
-size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t dk, int64_t dv, bool packed);
+size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed);
 
 constexpr float kL2Eps = 1e-6f;
 
