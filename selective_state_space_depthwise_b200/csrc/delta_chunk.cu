@@ -330,7 +330,6 @@ __global__ void __launch_bounds__(128, 6)
   }
   const Span sp = span_of(a, s);
   if (blockIdx.x == 0 && pt < 2) next[pt] = 0u;  // the walks handed out, pass 1 and 2
-  griddep_launch_dependents();  // the walk may set up; it waits for this grid before it reads the workspace
   if (c < 0 || kC * c >= sp.len) return;
   const int n = min(kC, sp.len - kC * c), tok = sp.t0 + kC * c;
 
@@ -358,6 +357,9 @@ __global__ void __launch_bounds__(128, 6)
   __syncthreads();
   tcgen05_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + M::kBar + 16);
+  // The walk may set up; it waits for this grid before it reads the workspace. Not before this block has its tensor
+  // memory: a walk's block takes all of an SM's and keeps it while it waits.
+  griddep_launch_dependents();
   if (pt == 96) {
     wait(full, 0, 31);
 #pragma unroll
