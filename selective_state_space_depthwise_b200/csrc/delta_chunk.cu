@@ -700,7 +700,11 @@ __device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int s
     const int longest = max(1, c.chunks[0]);
     const int per = (longest + tid) / (tid + 1);
     float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms);
-    if (tid > 0) cost = per < kCutLeast ? 3.0e38f : cost * 1.05f;
+    // Offsets that do not ascend name rows twice, and could ask for more segments than the workspace holds: no cut.
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += c.chunks[i];
+    const bool fits = total <= a.L / kC + n;
+    if (tid > 0) cost = per < kCutLeast || !fits ? 3.0e38f : cost * 1.05f;
     int best = tid;
     for (int m = 16; m > 0; m >>= 1) {
       const float oc = __shfl_xor_sync(0xffffffffu, cost, m);

@@ -410,3 +410,28 @@ def test_decode_offsets_past_32_bits():
     index = torch.tensor([slots - 1], dtype=torch.int32, device="cuda")
     out = api.delta_decode_step(**{n: t[:, 0] for n, t in x.items()}, state=pool, state_index=index)
     check(out[:, None], pool[-1:], *rule(**x, state=s0))
+
+
+def test_offsets_that_do_not_ascend_stay_inside_their_buffers():
+    """Offsets that name the whole buffer again and again are no valid packing, and their rows' results are not
+    specified; the call still ends, writes nothing behind its workspace, outputs and states, and leaves the next call
+    its results."""
+    T, n, G, H, dk, dv = 2100, 41, 1, 2, 128, 64
+    x = {m: t[0] for m, t in inputs((1, T), G, H, dk, dv, seed=77).items()}
+    cu = torch.tensor([T * (i % 2) for i in range(n + 1)], dtype=torch.int32, device="cuda")
+    need = api.delta_prefill_workspace_bytes(n, T, H, G, dk, dv, packed=True)
+    room = 1 << 20
+    ws = torch.full((need + room,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((T + 64, H, dv), 5.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.full((n + 8, H, dv, dk), 5.0, device="cuda")
+    api.delta_prefill(**x, cu_seqlens=cu, workspace=ws[:need], out=out[:T], state_out=st[:n])
+    api.check_device_error()
+    assert (ws[need:] == 0x5A).all() and (out[T:] == 5).all() and (st[n:] == 5).all()
+    assert (st[1:n:2] == 0).all()  # the empty ones
+    lens = [T - 100, 100]
+    cu = torch.tensor([0, lens[0], T], dtype=torch.int32, device="cuda")
+    got, st = api.delta_prefill(**x, cu_seqlens=cu, workspace=ws[:need])
+    at = 0
+    for i, m in enumerate(lens):
+        check(got[None, at:at + m], st[i:i + 1], *rule(**{k: t[None, at:at + m] for k, t in x.items()}))
+        at += m
