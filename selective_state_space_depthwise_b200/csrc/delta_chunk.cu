@@ -218,6 +218,114 @@ struct ChunkMaps {
   CUtensorMap q, k, v, out;
 };
 
+// --------------------------------------------------------------- segments ---
+// A long sequence with few heads leaves most SMs idle, so it may be walked in
+// segments at once. The state is linear in the one before it: S_{p+1} = S_p M_p
+// + H_p, H_p a segment's walk from zero and M_p its walk of the identity without
+// values. Pass 1 (states only, OUT = false) forms both for every segment that
+// needs them, segment 0 from the state given; delta_join_kernel folds them into
+// the segments' first states; pass 2 walks all segments. More than twice the
+// work of one walk, on more than twice the SMs.
+//
+// Sequences of one length are cut on the host (count segments of per chunks).
+// The lengths of packed ones are known on the device alone: there a block of the
+// prep works out the cut (delta_cut) and leaves it in the workspace. (With the
+// code for it in the walk itself, the walk has to spill: 13% slower.)
+struct Cut;
+struct Segments {
+  int count, per;   // 1: one walk
+  Cut* cut;         // packed: cut on the device
+  int items;        // walks of this launch, where the host knows them
+  float* S;         // [segment][head][d_value][d_key]: the segments' first states
+  float* M;         // [segment][head][d_key][d_key]
+  uint32_t* next;   // walks handed out beyond one per block: pass 1's, pass 2's
+  int walkers;      // walks of one segment of a sequence: its heads times the slices of d_value, or pairs of heads
+  int sms;
+};
+
+constexpr int kCutSeqs = 256;  // most packed sequences that are cut
+constexpr int kCutLeast = 8;   // least chunks of a segment of theirs
+// Sequences in the order of their lengths, the longest first, so that the last walks handed out are short. For each
+// place: the sequence, and the segments before it (all; those pass 1 walks from a state; those it walks from the
+// identity). `per`: chunks of a segment.
+struct Cut {
+  int all[kCutSeqs + 1], walk[kCutSeqs + 1], ident[kCutSeqs + 1];
+  int chunks[kCutSeqs], seq[kCutSeqs];
+  int per;
+};
+
+// Time of a packed batch in chunks, cut into segments of `per`: the longest walk or the work of all over the SMs,
+// whichever is more, for both passes; launches and the join as in choose_segments.
+__device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int walkers, int sms) {
+  float w1 = 0.0f, w2 = 0.0f;
+  for (int s = 0; s < n; ++s) {
+    const int segs = (c.chunks[s] + per - 1) / per;
+    w2 += static_cast<float>(c.chunks[s] * walkers);
+    if (segs > 1) w1 += static_cast<float>(((segs - 1) * walkers + (segs - 2) * heads) * per);
+  }
+  const float scale = 1.0f / static_cast<float>(sms), len = static_cast<float>(per);
+  const float second = fmaxf(len, w2 * scale + 0.3f * len) + 2.5f;
+  if (per >= longest) return second;
+  return 0.85f * fmaxf(len, w1 * scale + 0.3f * len) + second + 5.5f +
+         1.6f * static_cast<float>((longest + per - 1) / per - 2);
+}
+
+// All threads of a block, with `c` in shared memory; ends with a barrier.
+__device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int sms, Cut& c) {
+  const int n = static_cast<int>(a.batch), tid = threadIdx.x;
+  for (int s = tid; s < n; s += blockDim.x) c.all[s] = (span_of(a, s).len + kC - 1) / kC;
+  __syncthreads();
+  for (int s = tid; s < n; s += blockDim.x) {
+    int place = 0;
+    for (int i = 0; i < n; ++i) place += c.all[i] > c.all[s] || (c.all[i] == c.all[s] && i < s);
+    c.chunks[place] = c.all[s], c.seq[place] = s;
+  }
+  __syncthreads();
+  if (tid < 32) {  // lane l: the longest in l + 1 segments
+    const int longest = max(1, c.chunks[0]);
+    const int per = (longest + tid) / (tid + 1);
+    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms);
+    // Offsets that do not ascend name rows twice, and could ask for more segments than the workspace holds: no cut.
+    int64_t total = 0;
+    for (int i = 0; i < n; ++i) total += c.chunks[i];
+    const bool fits = total <= a.L / kC + n;
+    if (tid > 0) cost = per < kCutLeast || !fits ? 3.0e38f : cost * 1.05f;
+    int best = tid;
+    for (int m = 16; m > 0; m >>= 1) {
+      const float oc = __shfl_xor_sync(0xffffffffu, cost, m);
+      const int ob = __shfl_xor_sync(0xffffffffu, best, m);
+      if (oc < cost || (oc == cost && ob < best)) cost = oc, best = ob;
+    }
+    if (tid == 0) c.per = (longest + best) / (best + 1);
+  }
+  __syncthreads();
+  if (tid < 3) {
+    int* out = tid == 0 ? c.all : tid == 1 ? c.walk : c.ident;
+    int sum = 0;
+    for (int s = 0; s < n; ++s) {
+      out[s] = sum;
+      sum += max(max(1, (c.chunks[s] + c.per - 1) / c.per) - tid, 0);
+    }
+    out[n] = sum;
+  }
+  __syncthreads();
+}
+// `from` to `to`, by all threads of a block; no barrier.
+__device__ __forceinline__ void copy_cut(const Cut* from, Cut* to) {
+  for (int i = threadIdx.x; i < static_cast<int>(sizeof(Cut) / 4); i += blockDim.x)
+    reinterpret_cast<int*>(to)[i] = reinterpret_cast<const int*>(from)[i];
+}
+// The place that item i of a running sum belongs to.
+__device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (sums[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
 // ------------------------------------------------------------------- prep ---
 // One CTA of 4 warps per chunk and up to kPrepHeads heads of one key group.
 // Thread pt owns row pt of the 128 x 64 product [K; Q] K^T (one
@@ -300,7 +408,7 @@ __device__ __forceinline__ void block_store(float* D, int lane, const float (&c)
 template <int KA>
 __global__ void __launch_bounds__(128, 6)
     delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int head_sets,
-                      uint32_t* next) {
+                      const Segments sg) {
   using M = PrepSmem<KA>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -309,8 +417,15 @@ __global__ void __launch_bounds__(128, 6)
   const Shifter sh{a.two16};
   const int warp = __shfl_sync(0xffffffffu, pt >> 5, 0);
   const int rep = static_cast<int>(a.H / a.G);
-  const int set = static_cast<int>(blockIdx.x) % head_sets;
-  const int64_t gslot = blockIdx.x / head_sets;
+  if (blockIdx.x == 0 && pt < 2) sg.next[pt] = 0u;  // the walks handed out, pass 1 and 2
+  int block = static_cast<int>(blockIdx.x);
+  if (sg.cut && block-- == 0) {
+    delta_cut(a, sg.walkers, sg.sms, *reinterpret_cast<Cut*>(smem));
+    copy_cut(reinterpret_cast<const Cut*>(smem), sg.cut);
+    return;
+  }
+  const int set = block % head_sets;
+  const int64_t gslot = block / head_sets;
   const int grp = static_cast<int>(gslot % a.G);
   const int64_t slot = gslot / a.G;
   // the sequence and chunk of this slot
@@ -329,7 +444,6 @@ __global__ void __launch_bounds__(128, 6)
     s = static_cast<int>(slot / nc), c = static_cast<int>(slot % nc);
   }
   const Span sp = span_of(a, s);
-  if (blockIdx.x == 0 && pt < 2) next[pt] = 0u;  // the walks handed out, pass 1 and 2
   if (c < 0 || kC * c >= sp.len) return;
   const int n = min(kC, sp.len - kC * c), tok = sp.t0 + kC * c;
 
@@ -636,106 +750,6 @@ constexpr uint32_t kTmY = 320;    // Y, then U
 constexpr uint32_t kTmO = 384;    // Q S^T, then with the scores' product
 constexpr uint32_t kTmU = 448;    // U's two output terms
 
-// A long sequence with few heads leaves most SMs idle, so it may be walked in
-// segments at once. The state is linear in the one before it: S_{p+1} = S_p M_p
-// + H_p, H_p a segment's walk from zero and M_p its walk of the identity without
-// values. Pass 1 (states only, OUT = false) forms both for every segment that
-// needs them, segment 0 from the state given; delta_join_kernel folds them into
-// the segments' first states; pass 2 walks all segments. More than twice the
-// work of one walk, on more than twice the SMs.
-//
-// Sequences of one length are cut on the host (count segments of per chunks).
-// The lengths of packed ones are known on the device alone: with `cut`, every
-// block works out the same cut for itself (delta_cut).
-struct Segments {
-  int count, per;   // 1: one walk
-  int cut;          // packed: cut on the device
-  int items;        // walks of this launch, where the host knows them
-  float* S;         // [segment][head][d_value][d_key]: the segments' first states
-  float* M;         // [segment][head][d_key][d_key]
-  uint32_t* next;   // walks handed out beyond one per block: pass 1's, pass 2's
-  int walkers;      // walks of one segment of a sequence: its heads times the slices of d_value, or pairs of heads
-  int sms;
-};
-
-constexpr int kCutSeqs = 256;  // most packed sequences that are cut
-constexpr int kCutLeast = 8;   // least chunks of a segment of theirs
-// Sequences in the order of their lengths, the longest first, so that the last walks handed out are short. For each
-// place: the sequence, and the segments before it (all; those pass 1 walks from a state; those it walks from the
-// identity). `per`: chunks of a segment.
-struct Cut {
-  int all[kCutSeqs + 1], walk[kCutSeqs + 1], ident[kCutSeqs + 1];
-  int chunks[kCutSeqs], seq[kCutSeqs];
-  int per;
-};
-
-// Time of a packed batch in chunks, cut into segments of `per`: the longest walk or the work of all over the SMs,
-// whichever is more, for both passes; launches and the join as in choose_segments.
-__device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int walkers, int sms) {
-  float w1 = 0.0f, w2 = 0.0f;
-  for (int s = 0; s < n; ++s) {
-    const int segs = (c.chunks[s] + per - 1) / per;
-    w2 += static_cast<float>(c.chunks[s] * walkers);
-    if (segs > 1) w1 += static_cast<float>(((segs - 1) * walkers + (segs - 2) * heads) * per);
-  }
-  const float scale = 1.0f / static_cast<float>(sms), len = static_cast<float>(per);
-  const float second = fmaxf(len, w2 * scale + 0.3f * len) + 2.5f;
-  if (per >= longest) return second;
-  return 0.85f * fmaxf(len, w1 * scale + 0.3f * len) + second + 5.5f +
-         1.6f * static_cast<float>((longest + per - 1) / per - 2);
-}
-
-// All threads of a block; ends with a barrier.
-__device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int sms, Cut& c) {
-  const int n = static_cast<int>(a.batch), tid = threadIdx.x;
-  for (int s = tid; s < n; s += blockDim.x) c.all[s] = (span_of(a, s).len + kC - 1) / kC;
-  __syncthreads();
-  for (int s = tid; s < n; s += blockDim.x) {
-    int place = 0;
-    for (int i = 0; i < n; ++i) place += c.all[i] > c.all[s] || (c.all[i] == c.all[s] && i < s);
-    c.chunks[place] = c.all[s], c.seq[place] = s;
-  }
-  __syncthreads();
-  if (tid < 32) {  // lane l: the longest in l + 1 segments
-    const int longest = max(1, c.chunks[0]);
-    const int per = (longest + tid) / (tid + 1);
-    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms);
-    // Offsets that do not ascend name rows twice, and could ask for more segments than the workspace holds: no cut.
-    int64_t total = 0;
-    for (int i = 0; i < n; ++i) total += c.chunks[i];
-    const bool fits = total <= a.L / kC + n;
-    if (tid > 0) cost = per < kCutLeast || !fits ? 3.0e38f : cost * 1.05f;
-    int best = tid;
-    for (int m = 16; m > 0; m >>= 1) {
-      const float oc = __shfl_xor_sync(0xffffffffu, cost, m);
-      const int ob = __shfl_xor_sync(0xffffffffu, best, m);
-      if (oc < cost || (oc == cost && ob < best)) cost = oc, best = ob;
-    }
-    if (tid == 0) c.per = (longest + best) / (best + 1);
-  }
-  __syncthreads();
-  if (tid < 3) {
-    int* out = tid == 0 ? c.all : tid == 1 ? c.walk : c.ident;
-    int sum = 0;
-    for (int s = 0; s < n; ++s) {
-      out[s] = sum;
-      sum += max(max(1, (c.chunks[s] + c.per - 1) / c.per) - tid, 0);
-    }
-    out[n] = sum;
-  }
-  __syncthreads();
-}
-// The place that item i of a running sum belongs to.
-__device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (sums[mid] <= i) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
 template <int KA, bool PAIR>
 struct ChainSmem {
   static constexpr int kImgs = PAIR ? 2 : 1;  // heads
@@ -804,10 +818,13 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int row = 32 * (warp & 3) + lane;
   const int H = static_cast<int>(a.H), nseq = static_cast<int>(a.batch);
   Cut& cut = *reinterpret_cast<Cut*>(smem + M::kCut);
-  if (sg.cut) delta_cut(a, sg.walkers, sg.sms, cut);
+  griddep_wait();  // the prep's tiles, the counter of walks, the cut
+  if (sg.cut) {
+    copy_cut(sg.cut, &cut);
+    __syncthreads();
+  }
   const int walks = sg.cut ? cut.walk[nseq] * sg.walkers : nseq * sg.walkers * (sg.count - 1);
   const int items = !sg.cut ? sg.items : OUT ? cut.all[nseq] * sg.walkers : walks + cut.ident[nseq] * H;
-  griddep_wait();  // the prep's tiles, and the counter of walks
   // Walks until none is left. `done`: chunks of the walks before this one, so that the barriers' phases run on.
   int done = 0;
   for (int item = static_cast<int>(blockIdx.x); item < items;) {
@@ -1262,7 +1279,10 @@ __global__ void __launch_bounds__(128)
   float* Ss = join_smem + 2 * 128 * 128;  // S_p [row][key channel]
   const int H = static_cast<int>(a.H);
   Cut& cut = *reinterpret_cast<Cut*>(Ss + kJoinRows * kJoinLd);
-  if (sg.cut) delta_cut(a, sg.walkers, sg.sms, cut);
+  if (sg.cut) {
+    copy_cut(sg.cut, &cut);
+    __syncthreads();
+  }
   for (int item = static_cast<int>(blockIdx.x); item < static_cast<int>(a.batch) * H * row_blocks; item += gridDim.x) {
   const int sh = item / row_blocks, s = sh / H;  // with a cut: the place in its order, the longest first
   int count = sg.count, first_seg = s * count;
@@ -1351,7 +1371,7 @@ struct ChunkPlan {
   int64_t slots;
   int slices, walkers, count, per, sms;
   bool cut, pair;
-  size_t next, S, M, bytes;  // offsets behind the operand tiles, and the end
+  size_t next, cuts, S, M, bytes;  // offsets behind the operand tiles, and the end
 };
 ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed) {
   int dev = 0;
@@ -1375,7 +1395,8 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk,
     p.count = choose_segments(nc, batch * p.walkers, batch * H, dv, p.sms, &p.per);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.next = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
-  p.S = p.M = p.bytes = p.next + 256;
+  p.cuts = p.next + 256;
+  p.S = p.M = p.bytes = p.cuts + (p.cut ? up(sizeof(Cut)) : 0);
   if (p.count > 1 || p.cut) {
     const int64_t segs = p.cut ? p.slots / kCutLeast + batch : batch * p.count;
     p.M = up(p.S + static_cast<size_t>(segs * H * dv * dk) * 4);
@@ -1421,9 +1442,9 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   }
   const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
   const int64_t bh = a.batch * a.H, units = a.batch * p.walkers;
-  Segments sg{p.count, p.per, p.cut, static_cast<int>(units * p.count), reinterpret_cast<float*>(img + p.S),
+  Segments sg{p.count, p.per, p.cut ? reinterpret_cast<Cut*>(img + p.cuts) : nullptr, static_cast<int>(units * p.count), reinterpret_cast<float*>(img + p.S),
               reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), p.walkers, p.sms};
-  prep<<<static_cast<unsigned>(p.slots * a.G * sets), 128, prep_smem, st>>>(maps, a, img, sets, sg.next);
+  prep<<<static_cast<unsigned>(p.slots * a.G * sets + p.cut), 128, prep_smem, st>>>(maps, a, img, sets, sg);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   if (p.count == 1 && !p.cut) return launch_chain<KA, true, PAIR>(maps, a, img, p, sg, true, st);
