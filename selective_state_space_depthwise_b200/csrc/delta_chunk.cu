@@ -78,7 +78,7 @@ struct Coef {
 constexpr int kImgP = 3 * kPanelTerm, kImgCoef = 5 * kPanelTerm;
 constexpr int kImgBytes = kImgCoef + static_cast<int>(sizeof(Coef));
 constexpr int kImgStride = (kImgBytes + 127) / 128 * 128;
-static_assert(panel_off(1) == 2048 && panel_off(3) == 4608 && kImgBytes % 16 == 0, "panel layout");
+static_assert(panel_off(1) == 2048 && panel_off(3) == 4608 && kImgBytes % 16 == 0 && kImgBytes + 8 <= kImgStride, "panel layout");
 
 // 16-byte piece of row i, columns 8 j8 .. 8 j8 + 7 within a term's panels.
 __device__ __forceinline__ int panel_piece(int i, int j8) {
@@ -1371,7 +1371,7 @@ struct ChunkPlan {
   int64_t slots;
   int slices, walkers, count, per, sms;
   bool cut, pair;
-  size_t next, cuts, S, M, bytes;  // offsets behind the operand tiles, and the end
+  size_t next, cuts, S, M, bytes;  // offsets of what is not operand tiles, and the end
 };
 ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed) {
   int dev = 0;
@@ -1394,8 +1394,8 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk,
   else
     p.count = choose_segments(nc, batch * p.walkers, batch * H, dv, p.sms, &p.per);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  p.next = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
-  p.cuts = p.next + 256;
+  p.next = kImgBytes;  // behind the first slot's tiles, which leave room there
+  p.cuts = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
   p.S = p.M = p.bytes = p.cuts + (p.cut ? up(sizeof(Cut)) : 0);
   if (p.count > 1 || p.cut) {
     const int64_t segs = p.cut ? p.slots / kCutLeast + batch : batch * p.count;
