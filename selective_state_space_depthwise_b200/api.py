@@ -408,7 +408,28 @@ def _raw_stream(device, stream):
     if device != torch.cuda.current_device():
         raise RuntimeError(f"tensors are on cuda:{device}, but the current device is "
                            f"cuda:{torch.cuda.current_device()}: make the call under torch.cuda.device(...)")
-    return _current_raw_stream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _current_raw_stream(device)
+    if stream.device_index != device:
+        raise RuntimeError(f"tensors are on cuda:{device}, but the stream is on cuda:{stream.device_index}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A buffer of the call, allocated on its stream: once dropped, its memory goes to later work of that stream."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(workspace, nbytes, device, stream):
+    """The caller's workspace where it is large enough, else a new one."""
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        return _empty(nbytes, torch.uint8, device, stream)
+    return workspace
 
 
 def _address(t):
@@ -519,7 +540,7 @@ def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=Non
     if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
         raise ValueError("q must be [b, L, G, dk] and v [b, L, H, dv], or [tokens, ...] with cu_seqlens")
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     dev = _one_device("q k v g beta out state_in state_out cu_seqlens workspace", q, k, v, g, beta, out, state_in,
                       state_out, cu_seqlens, workspace)
     if packed:
@@ -535,13 +556,13 @@ def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=Non
     if state_in is not None:
         _delta_state("state_in", state_in, n, H, dv, dk)
     if state_out is None:
-        state_out = torch.empty((n, H, dv, dk), dtype=torch.float32, device=q.device)
+        state_out = _empty((n, H, dv, dk), torch.float32, q.device, stream)
     else:
         _delta_state("state_out", state_out, n, H, dv, dk)
     ref = ctypes.byref(d)
     ws = lib.ssm_delta_prefill_workspace_bytes(ref, 1 if packed else 0)
-    if ws and (workspace is None or workspace.numel() * workspace.element_size() < ws):
-        workspace = torch.empty(ws, dtype=torch.uint8, device=q.device)
+    if ws:
+        workspace = _workspace(workspace, ws, q.device, stream)
     st = lib.ssm_delta_prefill(ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
                                _address(cu_seqlens), _address(state_in), out.data_ptr(), state_out.data_ptr(),
                                workspace.data_ptr() if ws else None, ws, _raw_stream(dev, stream))
@@ -561,7 +582,7 @@ def delta_decode_step(q, k, v, g, beta, state, *, state_index=None, scale=None, 
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [b, G, dk] and v [b, H, dv]")
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if state_out is None:
         state_out = state
     dev = _one_device("q k v g beta state out state_out state_index", q, k, v, g, beta, state, out, state_out,
@@ -598,7 +619,7 @@ def gated_norm(x, z, weight, *, group_size=None, eps=1e-5, gate_first=False, out
     dim = shape[-1]
     group = dim if group_size is None else int(group_size)
     if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = _empty(shape, x.dtype, x.device, stream)
     dev = _one_device("x z out weight", x, z, out, weight)
     strides = []
     for name, t in (("x", x), ("z", z), ("out", out)):
@@ -643,9 +664,9 @@ def residual_norm(x, residual, weight, *, post_weight=None, residual_scale=1.0, 
     if rdt not in _DTYPES or (residual_dtype is not None and residual_dtype != rdt):
         raise ValueError("the residual must be float32 or bfloat16, of residual_dtype where that is given")
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=x.device)
+        out = _empty(shape, dt, x.device, stream)
     if residual_out is None:
-        residual_out = torch.empty(shape, dtype=rdt, device=x.device)
+        residual_out = _empty(shape, rdt, x.device, stream)
     dev = _one_device("x residual out residual_out weight post_weight", x, residual, out, residual_out, weight,
                       post_weight)
     strides = []
@@ -693,13 +714,13 @@ def residual_block_forward(x, residual, params, proj, norm_weight, *, post_weigh
     if residual_dtype not in _DTYPES:
         raise ValueError("the residual must be float32 or bfloat16")
     if residual_out is None:
-        residual_out = torch.empty((b, L, Dm), dtype=residual_dtype, device=dev)
+        residual_out = _empty((b, L, Dm), residual_dtype, dev, stream)
     if out is None:
-        out = torch.empty((b, L, Dm), dtype=torch.bfloat16, device=dev)
+        out = _empty((b, L, Dm), torch.bfloat16, dev, stream)
     if conv_cache_out is None:
-        conv_cache_out = torch.empty((b, 3, E), dtype=torch.bfloat16, device=dev)
+        conv_cache_out = _empty((b, 3, E), torch.bfloat16, dev, stream)
     if ssm_state_out is None:
-        ssm_state_out = torch.empty((b, E, 16), dtype=torch.float32, device=dev)
+        ssm_state_out = _empty((b, E, 16), torch.float32, dev, stream)
     full, cache, state = (b, L, Dm), (b, 3, E), (b, E, 16)
     for n, t, shape, dt in (("x", x, full, torch.bfloat16), ("residual", residual, full, residual_dtype),
                             ("residual_out", residual_out, full, residual_dtype), ("out", out, full, torch.bfloat16),
@@ -721,8 +742,7 @@ def residual_block_forward(x, residual, params, proj, norm_weight, *, post_weigh
     nw = _lib.SsmBlockNorm(norm_weight.data_ptr(), None if post_weight is None else post_weight.data_ptr(), eps,
                            residual_scale, _DTYPES[residual_dtype])
     ws = int(lib.ssm_residual_block_workspace_bytes(ctypes.byref(dims)))
-    if workspace is None or workspace.numel() * workspace.element_size() < ws:
-        workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, max(ws, 1), dev, stream)
     _need_cuda("workspace", workspace, dev)
     _lib.check(lib.ssm_residual_block_forward(
         ctypes.byref(dims), ctypes.byref(w), ctypes.byref(pw), ctypes.byref(nw), _ptr(x), _ptr(residual),

@@ -435,3 +435,23 @@ def test_offsets_that_do_not_ascend_stay_inside_their_buffers():
     for i, m in enumerate(lens):
         check(got[None, at:at + m], st[i:i + 1], *rule(**{k: t[None, at:at + m] for k, t in x.items()}))
         at += m
+
+
+@pytest.mark.parametrize("L", [300, 2500])
+def test_buffers_belong_to_the_calls_stream(L):
+    """With stream=, workspace and results are that stream's memory: what the current stream allocates right after the
+    call, while it still waits on its stream, is none of it."""
+    x = inputs((1, L), 1, 2, 128, 128, seed=L)
+    want = rule(**x)
+    api.delta_prefill(**x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ws = api.delta_prefill_workspace_bytes(1, L, 2, 1, 128, 128)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    out, st = api.delta_prefill(**x, stream=s)
+    for n in (ws, out.numel() * 2, st.numel() * 4):
+        for _ in range(4):
+            torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # the current stream writes over what it is given
+    torch.cuda.synchronize()
+    check(out, st, *want)

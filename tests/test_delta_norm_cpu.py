@@ -184,3 +184,11 @@ def test_residual_block_rejects_bad_arguments(lib):
                dict(ro=None), dict(out=None), dict(out=FAKE), dict(out=2 * FAKE), dict(ws=None), dict(ws=FAKE + 16),
                dict(nbytes=need - 1), dict(proj=_lib.SsmBlockWeights(FAKE, None, FAKE))):
         assert call(**kw) == _lib.SSM_ERR_INVALID_ARG, kw
+
+
+def test_a_workspace_must_be_contiguous():
+    """An expanded workspace has fewer bytes than elements."""
+    with pytest.raises(ValueError, match="contiguous"):
+        api._workspace(torch.empty(1, dtype=torch.uint8).expand(1024), 1024, torch.device("cpu"), None)
+    w = torch.empty(64, dtype=torch.uint8)
+    assert api._workspace(w, 64, w.device, None) is w and api._workspace(w, 65, w.device, None).numel() == 65
