@@ -467,10 +467,17 @@ typedef struct {
  *               last token; may be state_in
  *   workspace   ssm_delta_prefill_workspace_bytes() bytes of device scratch,
  *               256-byte aligned, or NULL when that is 0 (26 KB for each 64
- *               tokens and head, plus as much for each packed sequence). Calls
- *               that overlap on the GPU need separate workspaces.
+ *               tokens and head, plus as much for each packed sequence; calls
+ *               that may walk long sequences in segments keep a state and a
+ *               d_key x d_key matrix for each segment and head besides).
+ *               Calls that overlap on the GPU need separate workspaces.
  * A long sequence may be processed in pieces: feeding one call's state_out to
  * the next gives the result of one call up to fp32 rounding.
+ *
+ * Values that are not finite. From a token whose k (or its sum of squares in
+ * fp32), g or beta is not finite on, its head's outputs and state are not
+ * finite; of v, its row's; of q, only the token's output. Outputs before that
+ * token, other sequences and heads are unaffected.
  */
 /* Workspace of a call with these dims, with (packed = 1) or without cu_seqlens; 0 for invalid dims. */
 size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims *dims, int32_t packed);
@@ -625,7 +632,10 @@ ssm_status ssm_segment_carry(const ssm_dims *dims, const ssm_weights *w, const f
  * prefill's TMA ring, 2 the hand-overs of prefill kernel 5, 3-6 the block's x_proj kernel, 7-11 the chunk scan's
  * operand and MMA waits, 11 the decode's state ring, 21-29 the projection
  * GEMM (21 ring slot free, 22 accumulator free, 23 operands landed, 24
- * accumulator full, 25 and 29 drains, 27-28 the cut-tile handshake),
+ * accumulator full, 25 and 29 drains, 27-28 the cut-tile handshake), 31-32
+ * the delta rule's preparation of chunks (31 keys and queries landed, 32 their
+ * scores), 33-39 its walk (33 state, 34 tiles landed, 35 S K^T, 36 the
+ * updates, 38 S Q^T, 39 the outputs) and 40-47 the walk's control warp,
  * SSM_SELFTEST_WAIT_CODE the self-test below. Every kernel's waits give up
  * after about 2 s. */
 ssm_status ssm_check_device_error(void *stream);

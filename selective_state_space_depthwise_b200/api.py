@@ -423,6 +423,14 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty_like(t, stream):
+    """The same for a dense buffer of t's shape and type (half the host time of torch.empty)."""
+    if stream is None or not t.is_cuda:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _workspace(workspace, nbytes, device, stream):
     """The caller's workspace where it is large enough, else a new one."""
     if workspace is not None and not workspace.is_contiguous():
@@ -476,9 +484,6 @@ def _dense_heads(name, t):
         raise ValueError(f"the head and channel dimensions of {name} must be contiguous")
 
 
-_NO_STRIDES = (0,) * 10
-
-
 def _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, batch, seqlen, tokens, sequences):
     """Checks the token tensors of the delta rule ([..., heads, channels]; g, beta [..., heads]) and fills
     SsmDeltaDims; tokens, sequences: the dimensions that hold them, or None."""
@@ -498,7 +503,7 @@ def _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, batch, seqlen, tokens, 
         raise ValueError("scale must be positive")
     if q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous() and g.is_contiguous() \
             and beta.is_contiguous():
-        strides = _NO_STRIDES
+        strides = ()
     else:
         if H > 1 and g.numel() and (g.stride(-1) != 1 or beta.stride(-1) != 1):
             raise ValueError("the heads of g and beta must be contiguous")
@@ -540,7 +545,7 @@ def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=Non
     if q.dim() != (3 if packed else 4) or v.dim() != q.dim():
         raise ValueError("q must be [b, L, G, dk] and v [b, L, H, dv], or [tokens, ...] with cu_seqlens")
     if out is None:
-        out = _empty(v.shape, v.dtype, v.device, stream)
+        out = _empty_like(v, stream)
     dev = _one_device("q k v g beta out state_in state_out cu_seqlens workspace", q, k, v, g, beta, out, state_in,
                       state_out, cu_seqlens, workspace)
     if packed:
@@ -556,7 +561,8 @@ def delta_prefill(q, k, v, g, beta, *, state_in=None, cu_seqlens=None, scale=Non
     if state_in is not None:
         _delta_state("state_in", state_in, n, H, dv, dk)
     if state_out is None:
-        state_out = _empty((n, H, dv, dk), torch.float32, q.device, stream)
+        state_out = _empty((n, H, dv, dk), torch.float32, q.device, stream) if state_in is None \
+            else _empty_like(state_in, stream)
     else:
         _delta_state("state_out", state_out, n, H, dv, dk)
     ref = ctypes.byref(d)
@@ -582,7 +588,7 @@ def delta_decode_step(q, k, v, g, beta, state, *, state_index=None, scale=None, 
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q must be [b, G, dk] and v [b, H, dv]")
     if out is None:
-        out = _empty(v.shape, v.dtype, v.device, stream)
+        out = _empty_like(v, stream)
     if state_out is None:
         state_out = state
     dev = _one_device("q k v g beta state out state_out state_index", q, k, v, g, beta, state, out, state_out,
@@ -619,7 +625,7 @@ def gated_norm(x, z, weight, *, group_size=None, eps=1e-5, gate_first=False, out
     dim = shape[-1]
     group = dim if group_size is None else int(group_size)
     if out is None:
-        out = _empty(shape, x.dtype, x.device, stream)
+        out = _empty_like(x, stream)
     dev = _one_device("x z out weight", x, z, out, weight)
     strides = []
     for name, t in (("x", x), ("z", z), ("out", out)):
@@ -664,9 +670,10 @@ def residual_norm(x, residual, weight, *, post_weight=None, residual_scale=1.0, 
     if rdt not in _DTYPES or (residual_dtype is not None and residual_dtype != rdt):
         raise ValueError("the residual must be float32 or bfloat16, of residual_dtype where that is given")
     if out is None:
-        out = _empty(shape, dt, x.device, stream)
+        out = _empty_like(x, stream)
     if residual_out is None:
-        residual_out = _empty(shape, rdt, x.device, stream)
+        residual_out = _empty_like(residual, stream) if residual is not None and residual.shape == shape \
+            else _empty(shape, rdt, x.device, stream)
     dev = _one_device("x residual out residual_out weight post_weight", x, residual, out, residual_out, weight,
                       post_weight)
     strides = []

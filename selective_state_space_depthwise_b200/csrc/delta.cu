@@ -27,18 +27,15 @@
 namespace ssm {
 namespace {
 
-// Tokens from which sequences go to the chunk kernels: token by token a call of
-// 32 heads of 128 x 128 takes 0.58 us each (L = 16: 12 us), in chunks 17 us up to 64.
-constexpr int kChunkFrom = 26;
 constexpr int kRecWarps = 4;
 constexpr int kRecSteps = 8;  // row steps of a warp
 
-// Sums v[16] over the LPR lanes of a group. Lane i of the group returns entry
-// i (LPR = 16) or i / 2 (LPR = 32).
-template <int LPR>
-__device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
+// Sums v[N] over the LPR lanes of a group. Lane i of the group returns entry i / (LPR / N).
+template <int LPR, int N>
+__device__ __forceinline__ float reduce_all(float (&v)[N], int lane) {
+  int m = LPR / 2;
 #pragma unroll
-  for (int n = 16, m = LPR / 2; n > 1; n >>= 1, m >>= 1) {
+  for (int n = N; n > 1; n >>= 1, m >>= 1) {
     const bool hi = lane & m;
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {
@@ -46,7 +43,8 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane) {
       v[i] = keep + __shfl_xor_sync(0xffffffffu, give, m);
     }
   }
-  if (LPR == 32) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+#pragma unroll
+  for (; m > 0; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
   return v[0];
 }
 
@@ -69,12 +67,13 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 }
 
 // One block: kRecWarps * kRecSteps * 32 / LPR rows of one (sequence, head).
-// Seven blocks an SM: the registers that this leaves spill a little, but a
+// One token: seven blocks an SM: the registers that this leaves spill a little, but a
 // decode step of 256 x 60 heads of 128 x 128 (2.03 GB) takes 301 us (6.75
 // TB/s) against 311 with six, 338 with five and 306 with eight.
-template <int LPR>
-__global__ void __launch_bounds__(32 * kRecWarps, 7) delta_recurrent_kernel(const DeltaArgs a, int row_blocks) {
-  constexpr int kPar = 32 / LPR;  // rows of one step
+template <int LPR, int BLOCKS>
+__global__ void __launch_bounds__(32 * kRecWarps, BLOCKS) delta_recurrent_kernel(const DeltaArgs a, int row_blocks) {
+  constexpr int kPar = 32 / LPR;           // rows of one step
+  constexpr int kLanes = LPR / (2 * kRecSteps);  // lanes that hold one product
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t unit = blockIdx.x / row_blocks;
   const int64_t s = unit / a.H, h = unit % a.H;
@@ -102,13 +101,13 @@ __global__ void __launch_bounds__(32 * kRecWarps, 7) delta_recurrent_kernel(cons
   const __nv_bfloat16* kp = a.k + seq * a.k_seq + t0 * a.k_tok + grp * a.dk + c;
   const float* gp = a.g + seq * a.gb_seq + t0 * a.gb_tok + h;
   const float* bp = a.beta + seq * a.gb_seq + t0 * a.gb_tok + h;
-  // The reduction leaves product `mine` of the 16 here: p of step mine (< 8) or w of step mine - 8.
-  const int mine = (LPR == 32 ? lane >> 1 : lane) & 15, step = mine & 7;
+  // The reduction leaves product `mine` here: p of step mine (< kRecSteps) or w of step mine - kRecSteps.
+  const int mine = lane % LPR / kLanes, step = mine % kRecSteps;
   const int my_row = row0 + step * kPar + part;
   const bool row_in = my_row < a.dv;
   const __nv_bfloat16* vp = a.v + seq * a.v_seq + t0 * a.v_tok + h * a.dv + (row_in ? my_row : 0);
   __nv_bfloat16* op = a.out + seq * a.o_seq + t0 * a.o_tok + h * a.dv + my_row;
-  const bool stores = row_in && mine >= 8 && (LPR == 16 || !(lane & 1));
+  const bool stores = row_in && mine >= kRecSteps && lane % kLanes == 0;
 
   float4 S[kRecSteps];
   const int64_t sbase = (slot * a.H + h) * a.dv;
@@ -129,28 +128,28 @@ __global__ void __launch_bounds__(32 * kRecWarps, 7) delta_recurrent_kernel(cons
       qp += a.q_tok, kp += a.k_tok, vp += a.v_tok, gp += a.gb_tok, bp += a.gb_tok;
       qn = load_bf16x4(qp, in), kn = load_bf16x4(kp, in), gn = *gp, bn = *bp, vn = __bfloat162float(*vp);
     }
-    float rq = a.scale;
+    // The norms scale the products, not k and q: their sums are on the way while the products' are.
+    float rq = a.scale, rk = 1.0f;
     if (a.l2norm) {
-      const float rk = rsqrtf(group_sum<LPR>(dot4(k, k)) + kL2Eps);
+      rk = rsqrtf(group_sum<LPR>(dot4(k, k)) + kL2Eps);
       rq *= rsqrtf(group_sum<LPR>(dot4(q, q)) + kL2Eps);
-      k.x *= rk, k.y *= rk, k.z *= rk, k.w *= rk;
     }
-    const float kq = group_sum<LPR>(dot4(k, q));
+    const float kq = group_sum<LPR>(dot4(k, q)) * rk;
     const float decay = expf(g);
-    float pw[16];
+    float pw[2 * kRecSteps];
 #pragma unroll
-    for (int i = 0; i < kRecSteps; ++i) pw[i] = dot4(S[i], k), pw[8 + i] = dot4(S[i], q);
-    const float mine_sum = reduce16<LPR>(pw, lane);
-    const float u = b * (v - decay * mine_sum);  // meant by the lanes that hold a p
+    for (int i = 0; i < kRecSteps; ++i) pw[i] = dot4(S[i], k), pw[kRecSteps + i] = dot4(S[i], q);
+    const float mine_sum = reduce_all<LPR>(pw, lane);
+    const float u = b * (v - decay * (mine_sum * rk));  // meant by the lanes that hold a p
 #pragma unroll
     for (int i = 0; i < kRecSteps; ++i) {
-      const float ui = __shfl_sync(0xffffffffu, u, LPR == 32 ? 2 * i : part * 16 + i);
+      const float ui = __shfl_sync(0xffffffffu, u, part * LPR + kLanes * i) * rk;
       S[i].x = fmaf(decay, S[i].x, ui * k.x);
       S[i].y = fmaf(decay, S[i].y, ui * k.y);
       S[i].z = fmaf(decay, S[i].z, ui * k.z);
       S[i].w = fmaf(decay, S[i].w, ui * k.w);
     }
-    const float um = __shfl_sync(0xffffffffu, u, LPR == 32 ? 2 * step : part * 16 + step);
+    const float um = __shfl_sync(0xffffffffu, u, part * LPR + kLanes * step);
     if (stores) *op = __float2bfloat16_rn(rq * fmaf(decay, mine_sum, um * kq));
     op += a.o_tok;
     q = qn, k = kn, g = gn, b = bn, v = vn;
@@ -162,16 +161,25 @@ __global__ void __launch_bounds__(32 * kRecWarps, 7) delta_recurrent_kernel(cons
   }
 }
 
-cudaError_t launch_delta_recurrent(const DeltaArgs& a, cudaStream_t st) {
-  const int lpr = a.dk > 64 ? 32 : 16;
-  const int rows = kRecWarps * kRecSteps * (32 / lpr);
-  const int rb = static_cast<int>((a.dv + rows - 1) / rows);
-  const unsigned grid = static_cast<unsigned>(a.batch * a.H * rb);
-  if (lpr == 32)
-    delta_recurrent_kernel<32><<<grid, 32 * kRecWarps, 0, st>>>(a, rb);
-  else
-    delta_recurrent_kernel<16><<<grid, 32 * kRecWarps, 0, st>>>(a, rb);
+// Blocks of a (sequence, head).
+int64_t recurrent_blocks(int64_t dk, int64_t dv) {
+  const int64_t rows = kRecWarps * kRecSteps * (dk > 64 ? 1 : 2);
+  return (dv + rows - 1) / rows;
+}
+
+template <int LPR, int BLOCKS>
+cudaError_t launch_recurrent_as(const DeltaArgs& a, cudaStream_t st) {
+  const int rb = static_cast<int>(recurrent_blocks(a.dk, a.dv));
+  delta_recurrent_kernel<LPR, BLOCKS>
+      <<<static_cast<unsigned>(a.batch * a.H * rb), 32 * kRecWarps, 0, st>>>(a, rb);
   return cudaGetLastError();
+}
+
+// Over several tokens a block waits for its own sums, not for memory: four blocks an SM, whose registers hold it all
+// (16 tokens of 32 heads of 128 x 128 take 10.1 us, with seven 13.8; of 64 sequences 229 us against 233).
+cudaError_t launch_delta_recurrent(const DeltaArgs& a, cudaStream_t st) {
+  if (a.L > 1) return a.dk > 64 ? launch_recurrent_as<32, 4>(a, st) : launch_recurrent_as<16, 4>(a, st);
+  return a.dk > 64 ? launch_recurrent_as<32, 7>(a, st) : launch_recurrent_as<16, 7>(a, st);
 }
 
 ssm_status delta_shape(const ssm_delta_dims* d, bool prefill) {
@@ -195,8 +203,23 @@ ssm_status delta_shape(const ssm_delta_dims* d, bool prefill) {
   return SSM_OK;
 }
 
-// Whether a prefill takes the chunk kernels. Packed lengths are known on the device alone.
-bool takes_chunks(int64_t L, bool packed) { return L > 0 && (packed || L >= kChunkFrom); }
+// Whether a prefill takes the chunk kernels. Packed lengths are known on the device alone. Below 64 tokens token by
+// token may be faster, by these fits (us, within 15%) to 1 to 64 sequences of 8 to 80 heads: L tokens take 2.3 + L
+// (0.47 + 0.00145 for each block beyond one an SM); one chunk 17.5 (3 less up to 64 key channels, 2.5 more in pairs)
+// and 13 (16.5) for each further round of walks over the SMs. (32 heads of 128 x 128: 24 tokens 13.9, 33 18.3, in
+// chunks 17.7; 64 sequences of them: 8 tokens 131, 16 228, in chunks 180.)
+bool takes_chunks(const ssm_delta_dims& d, bool packed) {
+  if (d.seqlen <= 0) return false;
+  if (packed || d.seqlen >= kDeltaChunk) return true;
+  constexpr int64_t kSms = 148;
+  const int64_t blocks = d.batch * d.nheads * recurrent_blocks(d.d_key, d.d_value);
+  const int64_t rounds = (d.batch * delta_walkers(d.nheads, d.ngroups, d.d_value) + kSms - 1) / kSms;
+  const bool pair = delta_pairs(d.nheads, d.ngroups, d.d_value);
+  const double token = 0.47 + (blocks > kSms ? 0.00145 * static_cast<double>(blocks - kSms) : 0.0);
+  const double chunk = (pair ? 20.0 : 17.5) - (d.d_key <= 64 ? 3.0 : 0.0) +
+                       (pair ? 16.5 : 13.0) * static_cast<double>(rounds - 1);
+  return 2.3 + static_cast<double>(d.seqlen) * token > chunk;
+}
 
 // Shape, stride and pointer checks shared by both entry points.
 ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, const void* k, const void* v,
@@ -253,7 +276,7 @@ ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, cons
 extern "C" {
 
 size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims* dims, int32_t packed) {
-  if (ssm::delta_shape(dims, true) != SSM_OK || !ssm::takes_chunks(dims->seqlen, packed)) return 0;
+  if (ssm::delta_shape(dims, true) != SSM_OK || !ssm::takes_chunks(*dims, packed)) return 0;
   return ssm::delta_chunk_workspace(dims->batch, dims->seqlen, dims->nheads, dims->ngroups, dims->d_key, dims->d_value, packed);
 }
 
@@ -268,7 +291,7 @@ ssm_status ssm_delta_prefill(const ssm_delta_dims* dims, const void* q, const vo
   a.cu = cu_seqlens;
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t err;
-  if (ssm::takes_chunks(a.L, a.cu)) {
+  if (ssm::takes_chunks(*dims, a.cu)) {
     const size_t need = ssm::delta_chunk_workspace(a.batch, a.L, a.H, a.G, a.dk, a.dv, a.cu);
     if (!workspace || !ssm::aligned(workspace, 256))
       return fail(SSM_ERR_INVALID_ARG, "workspace is NULL or not 256-byte aligned");

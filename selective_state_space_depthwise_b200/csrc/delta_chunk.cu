@@ -57,7 +57,7 @@
 namespace ssm {
 namespace {
 
-constexpr int kC = 64;            // tokens of a chunk
+constexpr int kC = kDeltaChunk;   // tokens of a chunk
 constexpr int kAtom = kC * 128;   // 64 rows of 64 bf16: one swizzled operand atom
 
 // What the walk needs of a chunk and head, as the prep kernel leaves it: T in
@@ -327,7 +327,9 @@ __device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
 }
 
 // ------------------------------------------------------------------- prep ---
-// One CTA of 4 warps per chunk and up to kPrepHeads heads of one key group.
+// One CTA of 4 warps per chunk and up to kPrepHeads heads of one key group:
+// fewer where all of them still fit the SMs at once (64 tokens of 80 heads with
+// one group: 20 us, with four heads a block 29).
 // Thread pt owns row pt of the 128 x 64 product [K; Q] K^T (one
 // set of MMAs per CTA; tensor memory keeps it for all its heads): rows 0-63
 // give A, rows 64-127 the scores.
@@ -407,7 +409,7 @@ __device__ __forceinline__ void block_store(float* D, int lane, const float (&c)
 
 template <int KA>
 __global__ void __launch_bounds__(128, 6)
-    delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int head_sets,
+    delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int set_heads,
                       const Segments sg) {
   using M = PrepSmem<KA>;
   extern __shared__ unsigned char smem_raw[];
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(128, 6)
     copy_cut(reinterpret_cast<const Cut*>(smem), sg.cut);
     return;
   }
-  const int set = block % head_sets;
+  const int head_sets = (rep + set_heads - 1) / set_heads, set = block % head_sets;
   const int64_t gslot = block / head_sets;
   const int grp = static_cast<int>(gslot % a.G);
   const int64_t slot = gslot / a.G;
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(128, 6)
   float* rk = reinterpret_cast<float*>(smem + M::kRk);
   float* cfac = reinterpret_cast<float*>(smem + M::kCf);
   uint32_t* bad_tokens = reinterpret_cast<uint32_t*>(smem + M::kBar + 24);
-  const int h0 = grp * rep + set * kPrepHeads, nh = min(kPrepHeads, rep - set * kPrepHeads);
+  const int h0 = grp * rep + set * set_heads, nh = min(set_heads, rep - set * set_heads);
   // Warp w: head h0 + w. Running sums of g in log2 units and fp64, kept as two
   // floats, so that differences of far sums stay exact; a decay below 2^-256 is 0 anyway.
   if (warp < nh) {
@@ -1384,9 +1386,8 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk,
   }
   p.slots = chunk_slots(batch, L, packed);
   p.slices = static_cast<int>((dv + 127) / 128);
-  // Heads of 64 channels: two that share their keys fill the 128 rows of a walk.
-  p.pair = dv == 64 && H / G % 2 == 0;
-  p.walkers = p.pair ? static_cast<int>(H / 2) : static_cast<int>(H) * p.slices;
+  p.pair = delta_pairs(H, G, dv);
+  p.walkers = static_cast<int>(delta_walkers(H, G, dv));
   const int64_t nc = (L + kC - 1) / kC;
   p.count = 1, p.per = static_cast<int>(nc);
   if (packed)  // some sequence may be long enough to cut
@@ -1440,11 +1441,14 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
     if (err != cudaSuccess) return err;
     if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
-  const int rep = static_cast<int>(a.H / a.G), sets = (rep + kPrepHeads - 1) / kPrepHeads;
+  const int64_t rep = a.H / a.G;
+  auto prep_blocks = [&](int heads) { return p.slots * a.G * ((rep + heads - 1) / heads); };
+  int set_heads = kPrepHeads;
+  while (set_heads > 1 && prep_blocks(set_heads / 2) <= 5 * p.sms) set_heads /= 2;  // five blocks fit an SM
   const int64_t bh = a.batch * a.H, units = a.batch * p.walkers;
   Segments sg{p.count, p.per, p.cut ? reinterpret_cast<Cut*>(img + p.cuts) : nullptr, static_cast<int>(units * p.count), reinterpret_cast<float*>(img + p.S),
               reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), p.walkers, p.sms};
-  prep<<<static_cast<unsigned>(p.slots * a.G * sets + p.cut), 128, prep_smem, st>>>(maps, a, img, sets, sg);
+  prep<<<static_cast<unsigned>(prep_blocks(set_heads) + p.cut), 128, prep_smem, st>>>(maps, a, img, set_heads, sg);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   if (p.count == 1 && !p.cut) return launch_chain<KA, true, PAIR>(maps, a, img, p, sg, true, st);

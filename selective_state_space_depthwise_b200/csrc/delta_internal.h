@@ -24,6 +24,15 @@ struct DeltaArgs {
   int* err;
 };
 
+constexpr int kDeltaChunk = 64;  // tokens of a chunk
+
+// Heads of 64 channels: two that share their keys fill the 128 rows of a walk.
+inline bool delta_pairs(int64_t H, int64_t G, int64_t dv) { return dv == 64 && H / G % 2 == 0; }
+// Walks of a sequence: its heads times the slices of 128 channels, or pairs of heads.
+inline int64_t delta_walkers(int64_t H, int64_t G, int64_t dv) {
+  return delta_pairs(H, G, dv) ? H / 2 : H * ((dv + 127) / 128);
+}
+
 // 64 tokens at a time on the tensor cores; a.L > 0.
 cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st);
 size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed);
