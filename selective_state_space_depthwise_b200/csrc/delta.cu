@@ -206,8 +206,9 @@ ssm_status delta_shape(const ssm_delta_dims* d, bool prefill) {
 // Whether a prefill takes the chunk kernels. Packed lengths are known on the device alone. Below 64 tokens token by
 // token may be faster, by these fits (us, within 15%) to 1 to 64 sequences of 8 to 80 heads: L tokens take 2.3 + L
 // (0.47 + 0.00145 for each block beyond one an SM); one chunk 17.5 (3 less up to 64 key channels, 2.5 more in pairs)
-// and 13 (16.5) for each further round of walks over the SMs. (32 heads of 128 x 128: 24 tokens 13.9, 33 18.3, in
-// chunks 17.7; 64 sequences of them: 8 tokens 131, 16 228, in chunks 180.)
+// and 13 (16.5) for each further round of walks over the SMs, and 2 are added for its second launch. (32 heads of 128
+// x 128: 24 tokens 13.9, 33 18.3, in chunks 17.7, but 21.8 and 26.3 call after call from the host; 64 sequences of
+// them: 8 tokens 131, 16 228, in chunks 180.)
 bool takes_chunks(const ssm_delta_dims& d, bool packed) {
   if (d.seqlen <= 0) return false;
   if (packed || d.seqlen >= kDeltaChunk) return true;
@@ -216,7 +217,7 @@ bool takes_chunks(const ssm_delta_dims& d, bool packed) {
   const int64_t rounds = (d.batch * delta_walkers(d.nheads, d.ngroups, d.d_value) + kSms - 1) / kSms;
   const bool pair = delta_pairs(d.nheads, d.ngroups, d.d_value);
   const double token = 0.47 + (blocks > kSms ? 0.00145 * static_cast<double>(blocks - kSms) : 0.0);
-  const double chunk = (pair ? 20.0 : 17.5) - (d.d_key <= 64 ? 3.0 : 0.0) +
+  const double chunk = (pair ? 22.0 : 19.5) - (d.d_key <= 64 ? 3.0 : 0.0) +
                        (pair ? 16.5 : 13.0) * static_cast<double>(rounds - 1);
   return 2.3 + static_cast<double>(d.seqlen) * token > chunk;
 }
