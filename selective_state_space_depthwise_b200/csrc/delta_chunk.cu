@@ -353,8 +353,10 @@ struct PrepSmem {
   static constexpr int kVec = KA * 2 * kAtom > kAEnd ? KA * 2 * kAtom : kAEnd;  // per head: Ghi, Glo, beta [64]
   static constexpr int kRk = kVec + kPrepHeads * 3 * kC * 4;  // 1 / |k| [64]
   static constexpr int kCf = kRk + kC * 4;            // column factors [3][64]
-  static constexpr int kBar = kCf + 3 * kC * 4;
-  static constexpr int kTotal = kBar + 32;  // full, done, TMEM address, abort flag, tokens not finite
+  // full, done, TMEM address, abort flag, tokens not finite: behind block row 1's 16 factors, where a row has room,
+  // so that six blocks fit an SM
+  static constexpr int kBar = kCf + 64;
+  static constexpr int kTotal = kCf + 3 * kC * 4;
 };
 
 // A fp32 value as two tf32 ones: 11 bits, and the rest (13 bits, of which the product reads 11).
@@ -675,16 +677,20 @@ __global__ void __launch_bounds__(128, 6)
       }
     }
     __syncthreads();
+    auto pair_sync = [&]() {  // constant barrier ids: a variable one reserves all 16, and four blocks take an SM's 64
+      if (warp < 2) named_bar_sync(1, 64);
+      else named_bar_sync(2, 64);
+    };
     {  // 16 -> 32: two pairs, two warps each; the unused block right of a pair's first holds A21 T11
       const int o = 32 * (warp >> 1), c0 = 8 * (warp & 1);
       float c[1][4];
       block_product<16, 1>(As + (o + 16) * kALd + o, As + o * kALd + o + c0, lane, c);
       block_store<1>(As + o * kALd + o + 16 + c0, lane, c, 1.0f);
-      named_bar_sync(1 + (warp >> 1), 64);
+      pair_sync();
       block_product<16, 1>(As + (o + 16) * kALd + o + 16, As + o * kALd + o + 16 + c0, lane, c);
       block_store<1>(As + (o + 16) * kALd + o + c0, lane, c, -1.0f);
       // that block is zero in T11 and T22, which the next products read
-      named_bar_sync(1 + (warp >> 1), 64);
+      pair_sync();
       const float zero[1][4] = {};
       block_store<1>(As + o * kALd + o + 16 + c0, lane, zero, 1.0f);
     }

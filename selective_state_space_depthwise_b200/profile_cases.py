@@ -6,6 +6,8 @@
     python -m selective_state_space_depthwise_b200.profile_cases ssd NAME
     python -m selective_state_space_depthwise_b200.profile_cases segment WORKLOAD [T]
     python -m selective_state_space_depthwise_b200.profile_cases gemm M N K
+    python -m selective_state_space_depthwise_b200.profile_cases delta SEQUENCES TOKENS GROUPS HEADS DK DV
+    python -m selective_state_space_depthwise_b200.profile_cases norms ROWS
 
 prefill: three launches of the named workload's prefill (optionally shortened
 to L tokens, optionally with an explicit kernel (3, 4 or 5) and decay path (0 auto,
@@ -14,7 +16,9 @@ prompt, then three decode steps at the decode workload's shape (batch 256,
 E=7680, 252 MB of state); block: three block forwards of the named block
 workload (optionally L tokens); segment: three segment summaries of the first
 T tokens (default L / 8) of the named workload, then three carries of 7 such
-summaries; gemm: three projection GEMMs C[M][N] = A[M][K] . W[N][K]^T (bf16). Inputs are drawn on the GPU; a capture skips the
+summaries; gemm: three projection GEMMs C[M][N] = A[M][K] . W[N][K]^T (bf16); delta: three gated delta rule prefills, or
+decode steps where TOKENS is 1; norms: three gated norms of [ROWS, 7680] in groups of 128 and three residual norms of
+[ROWS, 2560] with a fp32 residual. Inputs are drawn on the GPU; a capture skips the
 first two launches of the kernel it selects (ncu -s 2 -c 1 -k regex:...).
 """
 from __future__ import annotations
@@ -103,6 +107,33 @@ def gemm_case(M: int, N: int, K: int):
     print("gemm ok", M, N, K, float(C.float().abs().mean()))
 
 
+def delta_case(b: int, L: int, G: int, H: int, dk: int, dv: int):
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    rnd = lambda *shape: torch.randn(shape, device="cuda", generator=gen)  # noqa: E731
+    q, k, v = (rnd(b, L, h, d).to(torch.bfloat16) for h, d in ((G, dk), (G, dk), (H, dv)))
+    g, beta, state = -0.1 * rnd(b, L, H).abs(), rnd(b, L, H).sigmoid(), rnd(b, H, dv, dk)
+    for _ in range(3):
+        if L == 1:
+            out = api.delta_decode_step(q[:, 0], k[:, 0], v[:, 0], g[:, 0], beta[:, 0], state, qk_l2norm=True)
+        else:
+            out, _ = api.delta_prefill(q, k, v, g, beta, state_in=state, qk_l2norm=True)
+    torch.cuda.synchronize()
+    print("delta ok", (b, L, G, H, dk, dv), float(out.float().abs().mean()))
+
+
+def norms_case(rows: int):
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    xz = torch.randn((rows, 2 * 7680), device="cuda", generator=gen).to(torch.bfloat16)
+    w = torch.ones(7680, device="cuda")
+    x, r = xz[:, :2560].contiguous(), torch.randn((rows, 2560), device="cuda", generator=gen)
+    for _ in range(3):
+        y = api.gated_norm(xz[:, :7680], xz[:, 7680:], w[:128], group_size=128)
+    for _ in range(3):
+        y2, _ = api.residual_norm(x, r, w[:2560])
+    torch.cuda.synchronize()
+    print("norms ok", rows, float(y.float().abs().mean()), float(y2.float().abs().mean()))
+
+
 if __name__ == "__main__":
     if sys.argv[1] == "prefill":
         L = int(sys.argv[3]) if len(sys.argv) > 3 else 0
@@ -117,6 +148,10 @@ if __name__ == "__main__":
         segment_case(sys.argv[2], int(sys.argv[3]) if len(sys.argv) > 3 else 0)
     elif sys.argv[1] == "gemm":
         gemm_case(int(sys.argv[2]), int(sys.argv[3]), int(sys.argv[4]))
+    elif sys.argv[1] == "delta":
+        delta_case(*(int(v) for v in sys.argv[2:8]))
+    elif sys.argv[1] == "norms":
+        norms_case(int(sys.argv[2]))
     elif sys.argv[1] == "decode":
         decode_case(int(sys.argv[2]) if len(sys.argv) > 2 else 256)
     else:
