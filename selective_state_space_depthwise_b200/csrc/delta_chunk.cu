@@ -339,9 +339,12 @@ __device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
 // 16: two factors that the row and the column bring along, neither above 1
 // where g <= 0, so that a product underflows only where the decay does.
 //
-// The inverse of I + A: 16 x 16 diagonal blocks by substitution (a block per
-// warp, a column per lane), then twice the block below a pair of inverted
-// ones, T21 = -T22 (A21 T11), first for 16 and then for 32 rows.
+// The inverse of I + A: 8 x 8 diagonal blocks by substitution (two a warp, a
+// column per lane), then the block below a pair of inverted ones, T21 = -T22
+// (A21 T11), for 8, 16 and 32 rows. (16 x 16 blocks by substitution, whose rows
+// every lane reads: 403 us for 8 sequences of 64 chunks and 80 heads, not 385.)
+// Shared memory (0.6 of its bandwidth), instruction issue (0.57) and barriers
+// bound the kernel together.
 constexpr int kPrepHeads = 4;
 constexpr int kALd = 68;  // floats between rows of A (16-byte rows, conflict-free columns)
 
@@ -653,28 +656,50 @@ __global__ void __launch_bounds__(128, 6)
       put(j, f, true);
     }
     __syncthreads();
-    {  // diagonal blocks: warp w's, a column per lane (twice)
-      const int o = 16 * warp, col = lane & 15;
-      const float* Ab = As + o * (kALd + 1);
-      float x[16];
+    {  // rows 16 w .. of warp w: two 8 x 8 blocks, a column per lane (twice), then the block between them
+      const int o = 16 * warp, blk = o + (lane & 8), col = lane & 7;
+      const float* Ab = As + blk * (kALd + 1);
+      float x[8];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float acc[4] = {r == col ? 1.0f : 0.0f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < 8; ++r) {
+        float acc[2] = {r == col ? 1.0f : 0.0f, 0.f};
 #pragma unroll
         for (int k = 0; k < r; k += 4) {
           const float4 w = *reinterpret_cast<const float4*>(Ab + r * kALd + k);
           acc[0] = fmaf(-w.x, x[k], acc[0]);
           if (k + 1 < r) acc[1] = fmaf(-w.y, x[k + 1], acc[1]);
-          if (k + 2 < r) acc[2] = fmaf(-w.z, x[k + 2], acc[2]);
-          if (k + 3 < r) acc[3] = fmaf(-w.w, x[k + 3], acc[3]);
+          if (k + 2 < r) acc[0] = fmaf(-w.z, x[k + 2], acc[0]);
+          if (k + 3 < r) acc[1] = fmaf(-w.w, x[k + 3], acc[1]);
         }
-        x[r] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        x[r] = acc[0] + acc[1];
       }
       __syncwarp();
       if (lane < 16) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) As[(o + r) * kALd + o + col] = x[r];
+        for (int r = 0; r < 8; ++r) As[(blk + r) * kALd + blk + col] = x[r];
       }
+      __syncwarp();
+      const int g = lane >> 2, t = lane & 3;
+      float* Ao = As + o * kALd + o;
+      auto product8 = [&](const float* L, const float* R, float (&c)[4]) {  // 8 x 8 x 8 in the upper rows
+        uint32_t ah[4] = {}, al[4] = {}, bh[2], bl[2];
+        split_tf32(L[g * kALd + t], ah[0], al[0]);
+        split_tf32(L[g * kALd + t + 4], ah[2], al[2]);
+        split_tf32(R[t * kALd + g], bh[0], bl[0]);
+        split_tf32(R[(t + 4) * kALd + g], bh[1], bl[1]);
+        c[0] = c[1] = c[2] = c[3] = 0.0f;
+        mma_tf32(c, al, bh);
+        mma_tf32(c, ah, bl);
+        mma_tf32(c, ah, bh);
+      };
+      float c[4];
+      product8(Ao + 8 * kALd, Ao, c);
+      *reinterpret_cast<float2*>(Ao + g * kALd + 8 + 2 * t) = make_float2(c[0], c[1]);
+      __syncwarp();
+      product8(Ao + 8 * kALd + 8, Ao + 8, c);
+      __syncwarp();
+      *reinterpret_cast<float2*>(Ao + (g + 8) * kALd + 2 * t) = make_float2(-c[0], -c[1]);
+      *reinterpret_cast<float2*>(Ao + g * kALd + 8 + 2 * t) = make_float2(0.0f, 0.0f);
     }
     __syncthreads();
     auto pair_sync = [&]() {  // constant barrier ids: a variable one reserves all 16, and four blocks take an SM's 64
