@@ -479,9 +479,22 @@ def _row_stride(name, t):
 
 def _dense_heads(name, t):
     """The last two dimensions (head, channel) dense."""
-    h, c = t.shape[-2:]
-    if ((c > 1 and t.stride(-1) != 1) or (h > 1 and t.stride(-2) != c)) and t.numel():
+    sh, st = t.shape, t.stride()
+    if ((sh[-1] > 1 and st[-1] != 1) or (sh[-2] > 1 and st[-2] != sh[-1])) and t.numel():
         raise ValueError(f"the head and channel dimensions of {name} must be contiguous")
+
+
+def _delta_strides(name, t, tokens, sequences, heads=True):
+    """t's token and sequence strides for the C call (see _stride; dimension None: 0); with `heads`, its last two
+    dimensions (head, channel) must be dense."""
+    if not t.numel():
+        return 0, 0
+    if heads and not t.is_contiguous():
+        _dense_heads(name, t)
+    sh, st = t.shape, t.stride()
+    a = 0 if tokens is None or sh[tokens] <= 1 else st[tokens] or _stride(name, t, tokens)
+    b = 0 if sequences is None or sh[sequences] <= 1 else st[sequences] or _stride(name, t, sequences)
+    return a, b
 
 
 def _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, batch, seqlen, tokens, sequences):
@@ -507,14 +520,11 @@ def _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, batch, seqlen, tokens, 
     else:
         if H > 1 and g.numel() and (g.stride(-1) != 1 or beta.stride(-1) != 1):
             raise ValueError("the heads of g and beta must be contiguous")
-        strides = []
-        for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("g", g)):
-            if t is not g:
-                _dense_heads(name, t)
-            strides.append(0 if tokens is None else _stride(name, t, tokens))
-            strides.append(0 if sequences is None else _stride(name, t, sequences))
-        if [0 if d is None else _stride("beta", beta, d) for d in (tokens, sequences)] != strides[8:]:
+        gs = _delta_strides("g", g, tokens, sequences, False)
+        if _delta_strides("beta", beta, tokens, sequences, False) != gs:
             raise ValueError("g and beta must share strides")
+        strides = (*_delta_strides("q", q, tokens, sequences), *_delta_strides("k", k, tokens, sequences),
+                   *_delta_strides("v", v, tokens, sequences), *_delta_strides("out", out, tokens, sequences), *gs)
     return _lib.SsmDeltaDims(batch, seqlen, H, G, qs[-1], vs[-1], scale, 1 if qk_l2norm else 0, *strides)
 
 
