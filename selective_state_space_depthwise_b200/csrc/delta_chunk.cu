@@ -255,8 +255,10 @@ struct Cut {
 };
 
 // Time of a packed batch in chunks, cut into segments of `per`: the longest walk or the work of all over the SMs,
-// whichever is more, for both passes; launches and the join as in choose_segments.
-__device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int walkers, int sms) {
+// whichever is more, for both passes; launches as in choose_segments, and for each segment of the longest the join
+// (`join`: its blocks for one sequence, over the SMs).
+__device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int walkers, int sms,
+                                         float join) {
   float w1 = 0.0f, w2 = 0.0f;
   for (int s = 0; s < n; ++s) {
     const int segs = (c.chunks[s] + per - 1) / per;
@@ -267,7 +269,7 @@ __device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int long
   const float second = fmaxf(len, w2 * scale + 0.3f * len) + 2.5f;
   if (per >= longest) return second;
   return 0.85f * fmaxf(len, w1 * scale + 0.3f * len) + second + 5.5f +
-         1.6f * static_cast<float>((longest + per - 1) / per - 2);
+         (0.4f + 0.7f * join) * static_cast<float>((longest + per - 1) / per - 2);
 }
 
 // All threads of a block, with `c` in shared memory; ends with a barrier.
@@ -284,7 +286,8 @@ __device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int s
   if (tid < 32) {  // lane l: the longest in l + 1 segments
     const int longest = max(1, c.chunks[0]);
     const int per = (longest + tid) / (tid + 1);
-    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms);
+    const float join = static_cast<float>(static_cast<int>(a.H) * ((static_cast<int>(a.dv) + 15) / 16)) / static_cast<float>(sms);
+    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms, join);
     // Offsets that do not ascend name rows twice, and could ask for more segments than the workspace holds: no cut.
     int64_t total = 0;
     for (int i = 0; i < n; ++i) total += c.chunks[i];
@@ -1300,78 +1303,98 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 }
 
 // First states of segments 2 .. count - 1: S_{p+1} = S_p M_p + H_p, H_p lying
-// where S_{p+1} goes. One block per 32 rows of a (sequence, head) through all
-// segments, M_{p+1} on its way to shared memory while M_p is used (read from L2
-// inside the product instead, a step takes 16 us, not 4). A warp has 8 rows, a
-// lane 4 key channels of them; fp32 throughout.
-constexpr int kJoinRows = 32, kJoinLd = 132;
-constexpr int kJoinSmem = (2 * 128 * 128 + kJoinRows * kJoinLd) * 4 + static_cast<int>(sizeof(Cut));
-__global__ void __launch_bounds__(128)
+// where S_{p+1} goes. One block per R rows of a (sequence, head) through all
+// segments, M_{p+1} on its way to shared memory while M_p is used. A warp takes
+// every eighth four of the products' key channels for all R rows, so that M is
+// read once, and the eight sums are added in a fixed order; fp32 throughout.
+// (4 heads of 8192 tokens, 16 segments: 20.7 us; with 32 rows a block and a row
+// a warp, M read by every warp, 58 us.)
+constexpr int kJoinWarps = 8, kJoinLd = 132;
+template <int R>
+constexpr int kJoinSmem = (2 * 128 * 128 + R * kJoinLd + kJoinWarps * R * 128) * 4 + static_cast<int>(sizeof(Cut));
+template <int R>
+__global__ void __launch_bounds__(32 * kJoinWarps, 1)
     delta_join_kernel(const DeltaArgs a, const Segments sg, int row_blocks) {
   extern __shared__ __align__(16) float join_smem[];
-  float* Ss = join_smem + 2 * 128 * 128;  // S_p [row][key channel]
-  const int H = static_cast<int>(a.H);
-  Cut& cut = *reinterpret_cast<Cut*>(Ss + kJoinRows * kJoinLd);
+  float* Ss = join_smem + 2 * 128 * 128;                    // S_p [row][key channel]
+  float* parts = Ss + R * kJoinLd;                          // [warp][row][key channel]
+  Cut& cut = *reinterpret_cast<Cut*>(parts + kJoinWarps * R * 128);
+  const int H = static_cast<int>(a.H), dk = static_cast<int>(a.dk), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = 4 * lane;
+  const bool in = col < dk;
   if (sg.cut) {
     copy_cut(sg.cut, &cut);
     __syncthreads();
   }
   for (int item = static_cast<int>(blockIdx.x); item < static_cast<int>(a.batch) * H * row_blocks; item += gridDim.x) {
-  const int sh = item / row_blocks, s = sh / H;  // with a cut: the place in its order, the longest first
-  int count = sg.count, first_seg = s * count;
-  if (sg.cut) first_seg = cut.all[s], count = cut.all[s + 1] - first_seg;
-  if (count < 3) break;
-  const int dk = static_cast<int>(a.dk), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = item % row_blocks * kJoinRows + 8 * warp, col = 4 * lane;
-  const int nr = min(8, static_cast<int>(a.dv) - r0);  // rows of this warp, none or fewer behind the last
-  const bool in = col < dk;
-  const int64_t index = static_cast<int64_t>(first_seg) * H + sh % H, step = a.dv * a.dk * H;
-  float* S = sg.S + index * a.dv * a.dk + static_cast<int64_t>(r0) * dk + col;
-  const float* Mp = sg.M + index * dk * dk;
-  auto fetch = [&](int p) {  // M_p, p >= 1
-    if (p + 1 < count) {
-      const uint32_t dst = smem_u32(join_smem + (p & 1) * 128 * 128);
-      const float* src = Mp + static_cast<int64_t>(p) * H * dk * dk;
-      for (int i = threadIdx.x; i < dk * dk / 4; i += 128) cp_async_16(dst + 16 * i, src + 4 * i);
-    }
-    cp_async_commit();
-  };
-  auto load = [&](int p, float4 (&v)[8]) {  // S_p's or H_{p-1}'s part of this thread
+    const int sh = item / row_blocks, s = sh / H;  // with a cut: the place in its order, the longest first
+    int count = sg.count, first_seg = s * count;
+    if (sg.cut) first_seg = cut.all[s], count = cut.all[s + 1] - first_seg;
+    if (count < 3) break;
+    const int r0 = item % row_blocks * R, nr = min(R, static_cast<int>(a.dv) - r0);
+    const int64_t index = static_cast<int64_t>(first_seg) * H + sh % H, step = a.dv * a.dk * H;
+    float* S = sg.S + index * a.dv * a.dk + static_cast<int64_t>(r0) * dk + col;
+    const float* Mp = sg.M + index * dk * dk;
+    auto fetch = [&](int p) {  // M_p, p >= 1
+      if (p + 1 < count) {
+        const uint32_t dst = smem_u32(join_smem + (p & 1) * 128 * 128);
+        const float* src = Mp + static_cast<int64_t>(p) * H * dk * dk;
+        for (int i = threadIdx.x; i < dk * dk / 4; i += 32 * kJoinWarps) cp_async_16(dst + 16 * i, src + 4 * i);
+      }
+      cp_async_commit();
+    };
+    auto load = [&](int p, float4 (&v)[R / kJoinWarps]) {  // S_p's or H_{p-1}'s part of this thread: rows warp, warp + 8 ..
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      v[r] = r < nr && in ? *reinterpret_cast<const float4*>(S + p * step + r * dk) : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  fetch(1);
-  float4 acc[8];
-  load(1, acc);
-  for (int p = 1; p + 1 < count; ++p) {
-    fetch(p + 1);
-    float* mine = Ss + 8 * warp * kJoinLd;  // a warp reads its own rows only
+      for (int i = 0; i < R / kJoinWarps; ++i) {
+        const int r = warp + kJoinWarps * i;
+        v[i] = r < nr && in ? *reinterpret_cast<const float4*>(S + p * step + r * dk) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    fetch(1);
+    float4 mine[R / kJoinWarps];
+    load(1, mine);
+    for (int p = 1; p + 1 < count; ++p) {
+      fetch(p + 1);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) *reinterpret_cast<float4*>(mine + r * kJoinLd + col) = acc[r];
-    load(p + 1, acc);
-    cp_async_wait<1>();
-    __syncthreads();
-    const float* Ms = join_smem + (p & 1) * 128 * 128 + (in ? col : 0);
-#pragma unroll 2
-    for (int k = 0; k < dk; k += 4) {
-      float4 m[4];
+      for (int i = 0; i < R / kJoinWarps; ++i)
+        *reinterpret_cast<float4*>(Ss + (warp + kJoinWarps * i) * kJoinLd + col) = mine[i];
+      load(p + 1, mine);
+      cp_async_wait<1>();
+      __syncthreads();
+      const float* Ms = join_smem + (p & 1) * 128 * 128 + (in ? col : 0);
+      uint64_t acc[R][2] = {};
+#pragma unroll 1
+      for (int k = 4 * warp; k < dk; k += 4 * kJoinWarps) {
+        ulonglong2 m[4];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) m[z] = *reinterpret_cast<const float4*>(Ms + (k + z) * dk);
+        for (int z = 0; z < 4; ++z) m[z] = *reinterpret_cast<const ulonglong2*>(Ms + (k + z) * dk);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float4 w = *reinterpret_cast<const float4*>(mine + r * kJoinLd + k);
-        acc[r].x = fmaf(w.x, m[0].x, fmaf(w.y, m[1].x, fmaf(w.z, m[2].x, fmaf(w.w, m[3].x, acc[r].x))));
-        acc[r].y = fmaf(w.x, m[0].y, fmaf(w.y, m[1].y, fmaf(w.z, m[2].y, fmaf(w.w, m[3].y, acc[r].y))));
-        acc[r].z = fmaf(w.x, m[0].z, fmaf(w.y, m[1].z, fmaf(w.z, m[2].z, fmaf(w.w, m[3].z, acc[r].z))));
-        acc[r].w = fmaf(w.x, m[0].w, fmaf(w.y, m[1].w, fmaf(w.z, m[2].w, fmaf(w.w, m[3].w, acc[r].w))));
+        for (int r = 0; r < R; ++r) {
+          const float4 w = *reinterpret_cast<const float4*>(Ss + r * kJoinLd + k);
+          const float wz[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            acc[r][0] = ffma2(pk2(wz[z], wz[z]), m[z].x, acc[r][0]);
+            acc[r][1] = ffma2(pk2(wz[z], wz[z]), m[z].y, acc[r][1]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        *reinterpret_cast<ulonglong2*>(parts + (warp * R + r) * 128 + col) = make_ulonglong2(acc[r][0], acc[r][1]);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < R / kJoinWarps; ++i) {
+        const int r = warp + kJoinWarps * i;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(parts + (w * R + r) * 128 + col);
+          mine[i].x += v.x, mine[i].y += v.y, mine[i].z += v.z, mine[i].w += v.w;
+        }
+        if (r < nr && in) *reinterpret_cast<float4*>(S + (p + 1) * step + r * dk) = mine[i];
       }
     }
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-      if (r < nr && in) *reinterpret_cast<float4*>(S + (p + 1) * step + r * dk) = acc[r];
-    __syncthreads();  // M_p's buffer and the rows are free
-  }
+    __syncthreads();  // the next item's rows and M may overwrite these
   }
 }
 
@@ -1379,13 +1402,18 @@ int64_t chunk_slots(int64_t batch, int64_t L, bool packed) {
   return packed ? L / kC + batch : batch * ((L + kC - 1) / kC);
 }
 
+// Rows of a join block: eight where such blocks fit the SMs at once.
+int join_rows(int64_t seq_heads, int64_t dv, int sms) { return seq_heads * ((dv + 7) / 8) <= sms ? 8 : 16; }
+
 // Segments of a walk of nc chunks with `units` (sequence, head, slice) on
 // `sms` SMs, in units of a chunk's time (3.4 us): a wave of walks takes its
 // chunks (0.85 of them in pass 1) and 2.5 to start, the extra launches 3, the
-// join 1.6 a segment and wave of its blocks. (Times of 1 to 32 segments for 2 to
+// join 0.4 (0.52 of 16 rows) a segment and wave of its blocks. (Times of 1 to 32 segments for 2 to
 // 60 heads and 2048 to 32768 tokens: the choice is within 10% of the best.)
 int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int64_t dv, int sms, int* per) {
   auto waves = [sms](int64_t blocks) { return static_cast<double>((blocks + sms - 1) / sms); };
+  const int rows = join_rows(seq_heads, dv, sms);
+  const double join = (rows == 8 ? 0.4 : 0.52) * waves(seq_heads * ((dv + rows - 1) / rows));
   double best = 0.95 * (static_cast<double>(nc) + 2.5) * waves(units);
   int count = 1;
   *per = static_cast<int>(nc);
@@ -1394,7 +1422,7 @@ int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int64_t dv, in
     if ((nc + len - 1) / len != p) continue;
     const double w1 = waves(units * (p - 1) + seq_heads * (p - 2)), w2 = waves(units * p);
     const double cost = static_cast<double>(len) * (0.85 * w1 + w2) + 2.5 * (w1 + w2) + 3.0 +
-                        1.6 * static_cast<double>(p - 2) * waves(seq_heads * ((dv + kJoinRows - 1) / kJoinRows));
+                        join * static_cast<double>(p - 2);
     if (cost < best) best = cost, count = static_cast<int>(p), *per = static_cast<int>(len);
   }
   return count;
@@ -1468,7 +1496,8 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
     err = cudaFuncSetAttribute(prep, kAttr, prep_smem);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true, PAIR>, kAttr, smem);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false, PAIR>, kAttr, smem);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_join_kernel, kAttr, kJoinSmem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_join_kernel<8>, kAttr, kJoinSmem<8>);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_join_kernel<16>, kAttr, kJoinSmem<16>);
     if (err != cudaSuccess) return err;
     if (dev < 64) ready.fetch_or(uint64_t{1} << dev, std::memory_order_release);
   }
@@ -1488,9 +1517,10 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   err = launch_chain<KA, false, PAIR>(maps, a, img, p, first, true, st);
   if (err != cudaSuccess) return err;
   if (p.count > 2 || p.cut) {
-    const int rb = static_cast<int>((a.dv + kJoinRows - 1) / kJoinRows);
-    const int64_t blocks = bh * rb < p.sms ? bh * rb : p.sms;  // one an SM
-    delta_join_kernel<<<static_cast<unsigned>(blocks), 128, kJoinSmem, st>>>(a, sg, rb);
+    const int rows = join_rows(bh, a.dv, p.sms), rb = static_cast<int>((a.dv + rows - 1) / rows);
+    const unsigned blocks = static_cast<unsigned>(bh * rb < p.sms ? bh * rb : p.sms);  // one an SM
+    if (rows == 8) delta_join_kernel<8><<<blocks, 32 * kJoinWarps, kJoinSmem<8>, st>>>(a, sg, rb);
+    else delta_join_kernel<16><<<blocks, 32 * kJoinWarps, kJoinSmem<16>, st>>>(a, sg, rb);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
   return launch_chain<KA, true, PAIR>(maps, a, img, p, sg, false, st);
