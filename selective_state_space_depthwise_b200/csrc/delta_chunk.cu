@@ -31,8 +31,7 @@
 // Precision. q, k and v are bf16 and enter exactly; the key norms, decays and
 // beta are fp32 factors of rows and columns, never folded into a bf16 operand.
 // S, R, U and T are fp32 and go to the tensor cores as three bf16 terms (their
-// sum is exact), as many
-// products as pairs of terms above 2^-24. Only the output's own product takes
+// sum is exact), as many products as pairs of terms above 2^-24. Only the output's own product takes
 // two terms (2^-16, against its rounding to bf16). The tensor core adds into
 // fp32 accumulators with truncation, so the state itself is added up in fp32
 // registers, and the accumulators hold one chunk's contribution at a time.
@@ -346,8 +345,8 @@ __device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
 // column per lane), then the block below a pair of inverted ones, T21 = -T22
 // (A21 T11), for 8, 16 and 32 rows. (16 x 16 blocks by substitution, whose rows
 // every lane reads: 403 us for 8 sequences of 64 chunks and 80 heads, not 385.)
-// Shared memory (0.6 of its bandwidth), instruction issue (0.57) and barriers
-// bound the kernel together.
+// Shared memory's bandwidth (0.73 of it used) and instruction issue (0.64) bound
+// the kernel: 211 us for 8 sequences of 32 chunks and 80 heads, 500 MB.
 constexpr int kPrepHeads = 4;
 constexpr int kALd = 68;  // floats between rows of A (16-byte rows, conflict-free columns)
 
@@ -380,7 +379,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 // stride kALd), K a multiple of 8; two tf32 terms each, three products (the
 // dropped one is 2^-22). 16-row blocks are far below the 128 rows of a
 // tcgen05 product, and in fp32 FMAs their operands' loads take the SM's whole
-// shared-memory bandwidth (4096 chunks and heads: 69 us; so: 59 us).
+// shared-memory bandwidth (4096 chunks and heads: 69 us with them, 59 us so; by
+// now 53).
 template <int K, int NT>
 __device__ __forceinline__ void block_product(const float* L, const float* R, int lane, float (&c)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;
@@ -775,6 +775,10 @@ __global__ void __launch_bounds__(128, 6)
 //               and the sum is rounded and stored a chunk later;
 //   warp 16     one thread issues the loads (two chunks in flight) and every MMA.
 // (Output warps of their own, 21 in all, leave 80 registers a thread: spills.)
+//
+// Bound by the chain through a chunk (state, Y, R, U, state), whose steps
+// alternate between the tensor cores (0.46 of the time busy) and the warps'
+// splits and scalings (issue 0.55): 3.4 us a chunk, 113 us for 2048 tokens.
 constexpr int kStateWarps = 16, kCtlWarp = 16;
 constexpr int kChainThreads = 32 * 17;
 constexpr int kStages = 2;
