@@ -541,7 +541,8 @@ ssm_status ssm_gated_norm(const ssm_gated_norm_dims *dims, const void *x, const 
  * x, y [rows, dim] io_dtype; residual_in, residual_out [rows, dim]
  * residual_dtype; row strides in elements (0 = dim); w, post_w [dim] fp32.
  * y is the norm of r' before its rounding to residual_dtype. residual_out may
- * be residual_in (same stride) and may be NULL (not written); y may be x.
+ * be residual_in (same stride) and may be NULL (not written); y may be x (same
+ * stride), but not residual_out.
  * dim <= 32768 (SSM_ERR_UNSUPPORTED above). Alignment as for ssm_gated_norm.
  */
 typedef struct {

@@ -1462,7 +1462,8 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk,
   p.cuts = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
   p.S = p.M = p.bytes = p.cuts + (p.cut ? up(sizeof(Cut)) : 0);
   if (p.count > 1 || p.cut) {
-    const int64_t segs = p.cut ? p.slots / kCutLeast + batch : batch * p.count;
+    // With a cut, only a sequence's last segment may be shorter than kCutLeast, and it has 32 segments at most.
+    const int64_t segs = !p.cut ? batch * p.count : batch + (p.slots / kCutLeast < 31 * batch ? p.slots / kCutLeast : 31 * batch);
     p.M = up(p.S + static_cast<size_t>(segs * H * dv * dk) * 4);
     p.bytes = up(p.M + static_cast<size_t>(segs * H * dk * dk) * 4);
   }

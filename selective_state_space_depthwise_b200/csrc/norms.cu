@@ -470,6 +470,7 @@ ssm_status ssm_residual_norm(const ssm_residual_norm_dims* d, const void* x, con
   if (d->rows == 0) return fail(SSM_OK, "");
   const size_t e = ssm::dtype_bytes(d->io_dtype), er = ssm::dtype_bytes(d->residual_dtype);
   if (!x || !w || !y) return fail(SSM_ERR_INVALID_ARG, "x, w or y is NULL");
+  if (y == residual_out) return fail(SSM_ERR_INVALID_ARG, "y and residual_out are the same buffer");
   if (!aligned(x, e) || !aligned(y, e) || !aligned(w, 4) || (post_w && !aligned(post_w, 4)) ||
       (residual_in && !aligned(residual_in, er)) || (residual_out && !aligned(residual_out, er)))
     return fail(SSM_ERR_INVALID_ARG, "a pointer is not aligned to its element");

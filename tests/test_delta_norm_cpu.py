@@ -150,6 +150,22 @@ def test_residual_norm_rejects_bad_arguments(lib):
     assert call(rows=0, x=None) == _lib.SSM_OK
 
 
+def test_residual_norm_refuses_one_buffer_for_both_results(lib):
+    """Both are bf16 here: the norm would be written over the sum."""
+    d = _lib.SsmResidualNormDims()
+    d.rows, d.dim, d.eps, d.residual_scale, d.io_dtype, d.residual_dtype = 4, 128, 1e-5, 1.0, 1, 1
+    st = lib.ssm_residual_norm(ctypes.byref(d), FAKE, FAKE, FAKE, None, 2 * FAKE, 2 * FAKE, None)
+    assert st == _lib.SSM_ERR_INVALID_ARG
+
+
+def test_packed_workspace_holds_32_segments_a_sequence_at_most(lib):
+    """The workspace of few long packed sequences grows with their chunks' tiles, not with their possible cuts."""
+    H, dk, dv = 4, 128, 128
+    chunk = 26496 * H  # tiles of 64 tokens
+    sizes = [api.delta_prefill_workspace_bytes(2, 64 * n, H, H, dk, dv, packed=True) for n in (4096, 8192)]
+    assert sizes[1] - sizes[0] == 4096 * chunk
+
+
 def test_norm_bindings_refuse_host_tensors_and_odd_rows(lib):
     x, w = torch.zeros(4, 64), torch.zeros(64)
     with pytest.raises(RuntimeError, match="CUDA tensor"):
