@@ -636,7 +636,8 @@ ssm_status ssm_segment_carry(const ssm_dims *dims, const ssm_weights *w, const f
  * accumulator full, 25 and 29 drains, 27-28 the cut-tile handshake), 31-32
  * the delta rule's preparation of chunks (31 keys and queries landed, 32 their
  * scores), 33-39 its walk (33 state, 34 tiles landed, 35 S K^T, 36 the
- * updates, 38 S Q^T, 39 the outputs) and 40-47 the walk's control warp,
+ * updates, 38 S Q^T, 39 the outputs), 40-47 the walk's control warp, 48 the
+ * state that another block of the walk leaves,
  * SSM_SELFTEST_WAIT_CODE the self-test below. Every kernel's waits give up
  * after about 2 s. */
 ssm_status ssm_check_device_error(void *stream);

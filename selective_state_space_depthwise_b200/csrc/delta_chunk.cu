@@ -237,10 +237,46 @@ struct Segments {
   int items;        // walks of this launch, where the host knows them
   float* S;         // [segment][head][d_value][d_key]: the segments' first states
   float* M;         // [segment][head][d_key][d_key]
-  uint32_t* next;   // walks handed out beyond one per block: pass 1's, pass 2's
+  uint32_t* next;   // walks (beyond one per block) or shares handed out: pass 1's, pass 2's
+  uint32_t* flags;  // shares: [share] the last pass in which its first walk's state was left for the next share
+  int job, share;   // shares: chunks of a walk, and a block's part of the line of all walks; job 0: whole walks
   int walkers;      // walks of one segment of a sequence: its heads times the slices of d_value, or pairs of heads
   int sms;
 };
+
+// Shares. Walks of one length, more than the SMs, are not handed out whole (320
+// walks on 148 SMs would take three rounds, not 2.2) but laid end to end on a
+// line that is cut into equal shares, one a block. A walk across a cut begins in
+// the share before it and ends in the one behind: a block starts with the last
+// walk of its share and ends with the first, so that its first item waits for
+// nothing, and its last for the first item of the share before, begun long ago.
+// Shares are handed out in order: what a block waits for is always running.
+// (8 sequences of 64 chunks, 80 heads in pairs: 723 us whole, 588 so; 32 heads of
+// 512 chunks in segments: both passes 937 and 827.) SHARE is a kernel of its own:
+// one that did both ways would walk whole ones 8% slower.
+constexpr int kStartChunks = 2;  // what starting a walk costs, in chunks
+constexpr int kShareLeast = 16;  // chunks of a walk that may be cut
+// The cut before share r: chunk `a` of walk `item`, on its first or last chunk where few would be left of one side.
+__device__ __forceinline__ void share_cut(const Segments& sg, int r, int& item, int& a) {
+  const int64_t x = static_cast<int64_t>(r) * sg.share;
+  const int width = sg.job + kStartChunks;
+  item = static_cast<int>(x / width);
+  a = static_cast<int>(x - static_cast<int64_t>(item) * width) - kStartChunks;
+  if (a < 4) a = 0;
+  if (a > sg.job - 4) a = sg.job;
+}
+// One thread: the item of share r before `item` (-1: its first); its chunks are c0 .. c1 - 1. -1 where there is none.
+__device__ __forceinline__ int3 share_item(const Segments& sg, int r, int items, int item) {
+  int i0, a0, i1, a1;
+  share_cut(sg, r, i0, a0);
+  share_cut(sg, r + 1, i1, a1);
+  int c0 = 0, c1 = sg.job;
+  if (item < 0 && a1 > 0 && i1 < items) item = i1, c1 = a1;
+  else item = min(item < 0 ? i1 : item, items) - 1;
+  if (item == i0) c0 = a0;
+  if (item < i0 || c0 >= sg.job) item = -1;
+  return make_int3(item, c0, c1);
+}
 
 constexpr int kCutSeqs = 256;  // most packed sequences that are cut
 constexpr int kCutLeast = 8;   // least chunks of a segment of theirs
@@ -427,7 +463,11 @@ __global__ void __launch_bounds__(128, 6)
   const Shifter sh{a.two16};
   const int warp = __shfl_sync(0xffffffffu, pt >> 5, 0);
   const int rep = static_cast<int>(a.H / a.G);
-  if (blockIdx.x == 0 && pt < 2) sg.next[pt] = 0u;  // the walks handed out, pass 1 and 2
+  if (blockIdx.x == 0) {
+    if (pt < 2) sg.next[pt] = 0u;  // the walks handed out, pass 1 and 2
+    if (sg.job)
+      for (int i = pt; i < sg.sms; i += 128) sg.flags[i] = 0u;
+  }
   int block = static_cast<int>(blockIdx.x);
   if (sg.cut && block-- == 0) {
     delta_cut(a, sg.walkers, sg.sms, *reinterpret_cast<Cut*>(smem));
@@ -802,19 +842,22 @@ struct ChainSmem {
   static constexpr int kBad = kOut + kOuts * kC * 256;   // int [4][128]
   static constexpr int kCut = kBad + 4 * 128 * 4;
   static constexpr int kBar = kCut + (static_cast<int>(sizeof(Cut)) + 15) / 16 * 16;
-  static constexpr int kMisc = kBar + (kStages + 16) * 8;  // TMEM address, abort flag, next item
-  static constexpr int kTotal = kMisc + 16;
+  static constexpr int kMisc = kBar + (kStages + 16) * 8;
+  static constexpr int kTotal = kMisc + 64;  // TMEM address, abort flag, from 8 on the item (enum Plan)
   static_assert(kTotal + 1024 <= 232448, "227 KB of shared memory");
   static constexpr uint32_t kTx = static_cast<uint32_t>(kImg + kImgs * kImgBytes);
 };
 
+// A block's item, in shared memory: the walk (-1: none), its share, its chunks, and what it is a walk of. (In registers
+// through the walk they spill.)
+enum Plan { kItem, kShare, kFrom, kTo, kSeq, kHead, kSlice, kSeg, kCount, kFirstSeg, kIdent };
 enum Bar {  // after the stages' full barriers; each completes once a chunk
   kSReady0, kSReady1, kSReady2, kSReady3, kYDone, kOiDone, kRReady, kUDone, kUsReady, kSDone0, kSDone1, kUoReady, kOiRead,
   kOaDone, kOFree, kNumNamed
 };
 static_assert(kNumNamed <= 15, "barrier count");
 
-template <int KA, bool OUT, bool PAIR>
+template <int KA, bool OUT, bool PAIR, bool SHARE>
 __global__ void __launch_bounds__(kChainThreads, 1)
     delta_chain_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, const unsigned char* img0,
                        int slices, const Segments sg) {
@@ -867,36 +910,70 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   const int items = !sg.cut ? sg.items : OUT ? cut.all[nseq] * sg.walkers : walks + cut.ident[nseq] * H;
   // Walks until none is left. `done`: chunks of the walks before this one, so that the barriers' phases run on.
   int done = 0;
-  for (int item = static_cast<int>(blockIdx.x); item < items;) {
-  // This walk's sequence, head, rows and segment; `ident`: of the identity.
-  const bool ident = !OUT && item >= walks;
-  int slice, h, s, seg = 0, count = sg.count, first_seg = 0;  // first_seg: the sequence's first segment
-  {
-    int i = ident ? item - walks : item;
-    const int sl = ident ? 1 : slices, heads = PAIR && !ident ? H / 2 : H;
-    if (sg.cut) {
-      slice = i % sl, i /= sl;
-      h = i % heads, i /= heads;
-      const int* sums = ident ? cut.ident : OUT ? cut.all : cut.walk;
-      const int place = cut_find(sums, nseq, i);
-      s = cut.seq[place];
-      seg = i - sums[place] + (ident ? 1 : 0);
-      count = cut.all[place + 1] - cut.all[place];
-      first_seg = cut.all[place];
+  volatile int* plan = reinterpret_cast<volatile int*>(smem + M::kMisc + 8);
+  if (tid == 0) plan[kItem] = -2;
+  for (;;) {
+  if (tid == 0) {  // the next item
+    int item = plan[kItem];
+    int3 p;
+    if constexpr (SHARE) {
+      if (item == -2) {
+        plan[kShare] = static_cast<int>(atomicAdd(sg.next + (OUT ? 1 : 0), 1u));
+        item = -1;
+      } else if (plan[kTo] < sg.job) {  // the state of this walk is left for the next share; its writes are behind a barrier
+        __threadfence();
+        atomicExch(sg.flags + plan[kShare], OUT ? 2u : 1u);
+      }
+      p = share_item(sg, plan[kShare], items, item);
     } else {
-      const int segs = OUT ? count : ident ? count - 2 : count - 1;
-      seg = i % segs + (ident ? 1 : 0), i /= segs;
-      slice = i % sl, i /= sl;
-      h = i % heads, s = i / heads;
-      first_seg = s * count;
+      if (item == -2) item = static_cast<int>(blockIdx.x);
+      else if (items > static_cast<int>(gridDim.x)) item = static_cast<int>(gridDim.x + atomicAdd(sg.next + (OUT ? 1 : 0), 1u));
+      else item = items;
+      p = make_int3(item < items ? item : -1, 0, 0x7fffffff);
+    }
+    plan[kItem] = p.x, plan[kFrom] = p.y, plan[kTo] = p.z;
+    if (p.x >= 0) {
+      const bool id = !OUT && p.x >= walks;
+      int i = id ? p.x - walks : p.x;
+      const int sl = id ? 1 : slices, heads = PAIR && !id ? H / 2 : H;
+      plan[kIdent] = id;
+      if (sg.cut) {
+        plan[kSlice] = i % sl, i /= sl;
+        plan[kHead] = i % heads, i /= heads;
+        const int* sums = id ? cut.ident : OUT ? cut.all : cut.walk;
+        const int place = cut_find(sums, nseq, i);
+        plan[kSeq] = cut.seq[place];
+        plan[kSeg] = i - sums[place] + (id ? 1 : 0);
+        plan[kCount] = cut.all[place + 1] - cut.all[place];
+        plan[kFirstSeg] = cut.all[place];
+      } else {
+        const int segs = OUT ? sg.count : id ? sg.count - 2 : sg.count - 1;
+        plan[kSeg] = i % segs + (id ? 1 : 0), i /= segs;
+        plan[kSlice] = i % sl, i /= sl;
+        plan[kHead] = i % heads, i /= heads;
+        plan[kSeq] = i;
+        plan[kCount] = sg.count;
+        plan[kFirstSeg] = i * sg.count;
+      }
     }
   }
+  __syncthreads();
+  if (plan[kItem] < 0) break;
+  // This walk's sequence, head, rows and segment; `ident`: of the identity; first_seg: the sequence's first segment.
+  const bool ident = !OUT && plan[kIdent];
+  const int slice = plan[kSlice], h = plan[kHead], s = plan[kSeq], seg = plan[kSeg], count = plan[kCount];
+  const int first_seg = plan[kFirstSeg];
   const int per = sg.cut ? cut.per : sg.per;
   Span sp = span_of(a, s);
-  const int64_t slot0 = slot_of(a, s, sp.t0) + static_cast<int64_t>(seg) * per;
+  const int64_t slot0 = slot_of(a, s, sp.t0) + static_cast<int64_t>(seg) * per + (SHARE ? plan[kFrom] : 0);
   if (count > 1) {
     sp.t0 += kC * per * seg;
     sp.len = max(0, min(sp.len - kC * per * seg, kC * per));
+  }
+  if constexpr (SHARE) {
+    const int c0 = plan[kFrom];
+    sp.t0 += kC * c0;
+    sp.len = max(0, min(sp.len - kC * c0, kC * (plan[kTo] - c0)));
   }
   const int nc = (sp.len + kC - 1) / kC;
   // With PAIR, h is a pair of heads: rows 0-63 head 2 h, rows 64-127 head 2 h + 1. The identity is one head's.
@@ -925,14 +1002,38 @@ __global__ void __launch_bounds__(kChainThreads, 1)
         from = nullptr;
       }
     }
+    // Where this walk's state is left for the next share: where it goes in the end, or over the segment's first state.
+    auto handed = [&]() -> float* {
+      const int64_t at_seg = plan[kFirstSeg] + plan[kSeg];
+      if (!OUT && plan[kIdent]) return sg.M + (at_seg * H + plan[kHead]) * a.dk * a.dk;
+      const int64_t head = PAIR ? 2 * plan[kHead] : plan[kHead];
+      if (OUT && plan[kCount] == 1) return a.state_out + (plan[kSeq] * a.H + head) * a.dv * a.dk;
+      return sg.S + ((at_seg + (OUT ? 0 : 1)) * H + head) * a.dv * a.dk;
+    };
+    const bool begun = SHARE && plan[kFrom] > 0;
+    if (begun) {
+      from = handed();
+      if (lane == 0) {
+        const volatile uint32_t* flag = sg.flags + plan[kShare] - 1;
+        const uint64_t w0 = globaltimer_ns();
+        while (*flag < (OUT ? 2u : 1u) && !*abort) {
+          if (globaltimer_ns() - w0 > 2000000000ull) {
+            *abort = 1;
+            if (a.err) atomicExch(a.err, 48);
+          }
+        }
+      }
+      __syncwarp();
+      __threadfence();
+    }
     uint64_t S[QC / 2];
 #pragma unroll
     for (int i = 0; i < QC; i += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (from && row_in && i < cols) v = *reinterpret_cast<const float4*>(from + at + i);
-      if (!OUT && from && row_in && i < cols)  // state_out may be state_in: pass 2 reads a copy
+      if (!OUT && !begun && from && row_in && i < cols)  // state_out may be state_in: pass 2 reads a copy
         *reinterpret_cast<float4*>(seg_state + at + i) = v;
-      if (!OUT && ident) {
+      if (!OUT && ident && !begun) {
         const int d = r - quarter * QC - i;
         v = make_float4(d == 0, d == 1, d == 2, d == 3);
       }
@@ -1128,9 +1229,11 @@ __global__ void __launch_bounds__(kChainThreads, 1)
 #pragma unroll
       for (int i0 = 0; i0 < QC; i0 += 16) update(i0);
     }
-    float* to = a.state_out + shi * one;
-    if (!OUT) to = ident ? sg.M + (static_cast<int64_t>(first_seg + seg) * H + h) * a.dk * a.dk : seg_state + H * one;
-    if (row_in && (!OUT || seg == count - 1)) {
+    const bool ends = !SHARE || plan[kTo] >= sg.job;
+    float* to = handed();
+    if (OUT && ends)
+      to = a.state_out + (static_cast<int64_t>(plan[kSeq]) * H + (PAIR ? 2 * plan[kHead] : plan[kHead])) * a.dv * a.dk;
+    if (row_in && (!OUT || !ends || plan[kSeg] == plan[kCount] - 1)) {
 #pragma unroll
       for (int i = 0; i < QC; i += 4)
         if (i < cols) {
@@ -1292,16 +1395,9 @@ __global__ void __launch_bounds__(kChainThreads, 1)
   }
   __syncwarp();
   tcgen05_fence_before();
-  if (tid == 0) {
-    int next = items;
-    if (items > static_cast<int>(gridDim.x)) next = static_cast<int>(gridDim.x + atomicAdd(sg.next + (OUT ? 1 : 0), 1u));
-    *reinterpret_cast<volatile int*>(smem + M::kMisc + 8) = next;
-  }
   __syncthreads();
   tcgen05_fence_after();
-  item = *reinterpret_cast<volatile int*>(smem + M::kMisc + 8);
   done += nc;
-  __syncthreads();
   }
   if (warp == kCtlWarp) tmem_dealloc(tmem, 512);
 }
@@ -1409,24 +1505,33 @@ int64_t chunk_slots(int64_t batch, int64_t L, bool packed) {
 // Rows of a join block: eight where such blocks fit the SMs at once.
 int join_rows(int64_t seq_heads, int64_t dv, int sms) { return seq_heads * ((dv + 7) / 8) <= sms ? 8 : 16; }
 
+// Time of `walks` walks of len chunks on `sms` SMs, in chunks (3.4 us): whole ones in rounds, each with 2.5 to start,
+// or equal shares of them (8% slower, and 3 for the hand-over), whichever is less. scale: of a chunk, 0.85 in pass 1.
+double walk_time(int64_t walks, int64_t len, int sms, double scale, bool* shares) {
+  const double whole = static_cast<double>((walks + sms - 1) / sms) * (scale * static_cast<double>(len) + 2.5);
+  const double shared = static_cast<double>(walks) / sms * (1.08 * scale * static_cast<double>(len) + 2.5) + 3.0;
+  *shares = walks > sms && len >= kShareLeast && shared < whole;
+  return *shares ? shared : whole;
+}
+
 // Segments of a walk of nc chunks with `units` (sequence, head, slice) on
-// `sms` SMs, in units of a chunk's time (3.4 us): a wave of walks takes its
-// chunks (0.85 of them in pass 1) and 2.5 to start, the extra launches 3, the
-// join 0.4 (0.52 of 16 rows) a segment and wave of its blocks. (Times of 1 to 32 segments for 2 to
-// 60 heads and 2048 to 32768 tokens: the choice is within 10% of the best.)
+// `sms` SMs: the time of both passes, 3 for the extra launches, and for each
+// segment and wave of the join's blocks 0.4 (0.52 of 16 rows). (Times of 1 to
+// 32 segments for 2 to 60 heads and 2048 to 32768 tokens: the choice is within
+// 10% of the best.)
 int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int64_t dv, int sms, int* per) {
-  auto waves = [sms](int64_t blocks) { return static_cast<double>((blocks + sms - 1) / sms); };
+  bool shares;
   const int rows = join_rows(seq_heads, dv, sms);
-  const double join = (rows == 8 ? 0.4 : 0.52) * waves(seq_heads * ((dv + rows - 1) / rows));
-  double best = 0.95 * (static_cast<double>(nc) + 2.5) * waves(units);
+  const int64_t blocks = seq_heads * ((dv + rows - 1) / rows);
+  const double join = (rows == 8 ? 0.4 : 0.52) * static_cast<double>((blocks + sms - 1) / sms);
+  double best = 0.95 * walk_time(units, nc, sms, 1.0, &shares);
   int count = 1;
   *per = static_cast<int>(nc);
   for (int64_t p = 2; p <= 64 && 4 * p <= nc && units * p <= 64 * sms; ++p) {
     const int64_t len = (nc + p - 1) / p;
     if ((nc + len - 1) / len != p) continue;
-    const double w1 = waves(units * (p - 1) + seq_heads * (p - 2)), w2 = waves(units * p);
-    const double cost = static_cast<double>(len) * (0.85 * w1 + w2) + 2.5 * (w1 + w2) + 3.0 +
-                        join * static_cast<double>(p - 2);
+    const double cost = walk_time(units * (p - 1) + seq_heads * (p - 2), len, sms, 0.85, &shares) +
+                        walk_time(units * p, len, sms, 1.0, &shares) + 3.0 + join * static_cast<double>(p - 2);
     if (cost < best) best = cost, count = static_cast<int>(p), *per = static_cast<int>(len);
   }
   return count;
@@ -1436,7 +1541,7 @@ struct ChunkPlan {
   int64_t slots;
   int slices, walkers, count, per, sms;
   bool cut, pair;
-  size_t next, cuts, S, M, bytes;  // offsets of what is not operand tiles, and the end
+  size_t next, flags, cuts, S, M, bytes;  // offsets of what is not operand tiles, and the end
 };
 ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed) {
   int dev = 0;
@@ -1459,7 +1564,10 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk,
     p.count = choose_segments(nc, batch * p.walkers, batch * H, dv, p.sms, &p.per);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   p.next = kImgBytes;  // behind the first slot's tiles, which leave room there
-  p.cuts = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
+  p.flags = up(static_cast<size_t>(p.slots) * static_cast<size_t>(H) * kImgStride);
+  // room for the shares' flags where one length and enough walks may have them
+  const int64_t most = batch * p.count * (p.walkers + H);
+  p.cuts = p.flags + (!packed && most > p.sms ? up(static_cast<size_t>(p.sms) * 4) : 0);
   p.S = p.M = p.bytes = p.cuts + (p.cut ? up(sizeof(Cut)) : 0);
   if (p.count > 1 || p.cut) {
     // With a cut, only a sequence's last segment may be shorter than kCutLeast, and it has 32 segments at most.
@@ -1483,7 +1591,8 @@ cudaError_t launch_chain(const ChunkMaps& maps, const DeltaArgs& a, const unsign
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = after_prep ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, delta_chain_kernel<KA, OUT, PAIR>, maps, a, img, p.slices, sg);
+  return sg.job ? cudaLaunchKernelEx(&cfg, delta_chain_kernel<KA, OUT, PAIR, true>, maps, a, img, p.slices, sg)
+                : cudaLaunchKernelEx(&cfg, delta_chain_kernel<KA, OUT, PAIR, false>, maps, a, img, p.slices, sg);
 }
 
 template <int KA, bool PAIR>
@@ -1499,8 +1608,10 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
     constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
     err = cudaFuncSetAttribute(prep, kAttr, prep_smem);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true, PAIR>, kAttr, smem);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false, PAIR>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true, PAIR, true>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, true, PAIR, false>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false, PAIR, true>, kAttr, smem);
+    if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_chain_kernel<KA, false, PAIR, false>, kAttr, smem);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_join_kernel<8>, kAttr, kJoinSmem<8>);
     if (err == cudaSuccess) err = cudaFuncSetAttribute(delta_join_kernel<16>, kAttr, kJoinSmem<16>);
     if (err != cudaSuccess) return err;
@@ -1512,13 +1623,25 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   while (set_heads > 1 && prep_blocks(set_heads / 2) <= 5 * p.sms) set_heads /= 2;  // five blocks fit an SM
   const int64_t bh = a.batch * a.H, units = a.batch * p.walkers;
   Segments sg{p.count, p.per, p.cut ? reinterpret_cast<Cut*>(img + p.cuts) : nullptr, static_cast<int>(units * p.count), reinterpret_cast<float*>(img + p.S),
-              reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), p.walkers, p.sms};
-  prep<<<static_cast<unsigned>(prep_blocks(set_heads) + p.cut), 128, prep_smem, st>>>(maps, a, img, set_heads, sg);
+              reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), reinterpret_cast<uint32_t*>(img + p.flags), 0, 0,
+              p.walkers, p.sms};
+  auto share = [&](Segments& g, double scale) {  // never for packed sequences
+    bool shares = false;
+    if (!a.cu) walk_time(g.items, p.per, p.sms, scale, &shares);
+    if (!shares) return;
+    g.job = p.per;
+    g.share = static_cast<int>((static_cast<int64_t>(g.items) * (p.per + kStartChunks) + p.sms - 1) / p.sms);
+  };
+  Segments first = sg;
+  first.items = static_cast<int>(units * (p.count - 1) + bh * (p.count - 2));
+  if (p.count > 1) share(first, 0.85);
+  share(sg, 1.0);
+  Segments both = sg;
+  both.job = sg.job | first.job;
+  prep<<<static_cast<unsigned>(prep_blocks(set_heads) + p.cut), 128, prep_smem, st>>>(maps, a, img, set_heads, both);
   err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   if (p.count == 1 && !p.cut) return launch_chain<KA, true, PAIR>(maps, a, img, p, sg, true, st);
-  Segments first = sg;
-  first.items = static_cast<int>(units * (p.count - 1) + bh * (p.count - 2));
   err = launch_chain<KA, false, PAIR>(maps, a, img, p, first, true, st);
   if (err != cudaSuccess) return err;
   if (p.count > 2 || p.cut) {

@@ -455,3 +455,22 @@ def test_buffers_belong_to_the_calls_stream(L):
             torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # the current stream writes over what it is given
     torch.cuda.synchronize()
     check(out, st, *want)
+
+
+@pytest.mark.parametrize("b,L,G,H,dk,dv", [
+    (3, 1100, 8, 64, 64, 128), (2, 1500, 1, 160, 128, 64), (11, 1024, 5, 15, 64, 72), (1, 1027, 3, 150, 32, 8),
+    (3, 2000, 2, 50, 128, 136), (1, 12000, 8, 32, 128, 128), (1, 12000, 2, 40, 64, 64),
+])
+def test_more_walks_than_sms(b, L, G, H, dk, dv):
+    """Walks that the blocks share: those cut between two of them continue from the state that the first leaves, with
+    a state given and updated in place, and call after call alike."""
+    x = inputs((b, L), G, H, dk, dv, seed=L + H, decay=0.05)
+    s0 = state0(b, H, dv, dk, L)
+    want = rule(**x, state=s0)
+    st = s0.clone()
+    out, _ = api.delta_prefill(**x, state_in=st, state_out=st)
+    api.check_device_error()
+    check(out, st, *want)
+    for _ in range(3):
+        again, st2 = api.delta_prefill(**x, state_in=s0)
+        assert torch.equal(again, out) and torch.equal(st2, st)
