@@ -47,7 +47,7 @@
 #include <atomic>
 
 #include "delta_internal.h"
-#include "sm100_ptx.cuh"
+#include "delta_ptx.cuh"
 #include "ssm.h"
 #include "ssm_internal.h"
 #include "ssm_math.cuh"

@@ -474,3 +474,49 @@ def test_more_walks_than_sms(b, L, G, H, dk, dv):
     for _ in range(3):
         again, st2 = api.delta_prefill(**x, state_in=s0)
         assert torch.equal(again, out) and torch.equal(st2, st)
+
+
+def test_shared_walks_at_once_and_replayed():
+    """Three calls with more walks than SMs at once, each on its own stream, and one captured and replayed while
+    another runs: blocks of one call wait for each other's states, never for another call."""
+    xs = [inputs((3, 1100), 8, 64, 64, 128, seed=90 + i, decay=0.05) for i in range(3)]
+    want = [api.delta_prefill(**x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[] for _ in xs]
+    for _ in range(4):
+        for i, (x, s) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(api.delta_prefill(**x))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for o, st in g:
+            assert torch.equal(o, w[0]) and torch.equal(st, w[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, st = api.delta_prefill(**xs[0])
+    for _ in range(3):
+        o.zero_(), st.zero_()
+        with torch.cuda.stream(streams[1]):
+            streams[1].wait_stream(torch.cuda.current_stream())
+            o1, st1 = api.delta_prefill(**xs[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0][0]) and torch.equal(st, want[0][1])
+        assert torch.equal(o1, want[1][0]) and torch.equal(st1, want[1][1])
+    api.check_device_error()
+
+
+def test_packed_on_the_edges_of_a_cut():
+    """Packed buffers where the first length to be cut, and 256 and 257 sequences, are just met."""
+    for lens in ([64 * 32 - 1], [64 * 31], [64 * 32, 64 * 8 + 1], [8] * 255 + [2100], [8] * 256 + [2100]):
+        T, H, dk, dv = sum(lens), 2, 64, 128
+        x = inputs((1, T), 1, H, dk, dv, seed=T, decay=0.05)
+        at = [0]
+        for n in lens:
+            at.append(at[-1] + n)
+        out, st = api.delta_prefill(**{m: t[0] for m, t in x.items()},
+                                    cu_seqlens=torch.tensor(at, dtype=torch.int32, device="cuda"))
+        for i in (0, len(lens) - 1):
+            want = rule(**{m: t[:, at[i]:at[i + 1]] for m, t in x.items()})
+            check(out[None, at[i]:at[i + 1]], st[i:i + 1], *want, f"sequence {i} of {len(lens)}")
