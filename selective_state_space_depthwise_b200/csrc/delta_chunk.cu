@@ -40,7 +40,9 @@
 // before theirs. Those of a token's k, g and beta (found by the prep) and of v
 // (found while the walk waits for a product) are taken out of the operands; the
 // state gets a NaN for them, and the outputs are NaN from the first such token
-// on. A state that is not finite makes its row's outputs so by itself.
+// on. A state that is not finite makes its row's outputs so by itself. Scores
+// that are not finite touch their token alone, but where two heads share a walk
+// they would meet the zeros in the other's rows, and are taken out too.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -181,6 +183,13 @@ __device__ __forceinline__ void store_split3(const Shifter& sh, uint32_t col, ui
   tmem_st_x8(col, h);
   tmem_st_x8(col + stride, m);
   tmem_st_x8(col + 2 * stride, l);
+}
+
+// a b + c of two bf16 each.
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
 
 __device__ __forceinline__ int sw128(int r, int j) { return r * 128 + ((j ^ (r & 7)) << 4); }
@@ -451,7 +460,7 @@ __device__ __forceinline__ void block_store(float* D, int lane, const float (&c)
   }
 }
 
-template <int KA>
+template <int KA, bool PAIR>
 __global__ void __launch_bounds__(128, 6)
     delta_prep_kernel(const __grid_constant__ ChunkMaps maps, const DeltaArgs a, unsigned char* img0, int set_heads,
                       const Segments sg) {
@@ -632,6 +641,7 @@ __global__ void __launch_bounds__(128, 6)
     const uint64_t bad_mask = bad_tokens[0] | static_cast<uint64_t>(bad_tokens[1]) << 32;
     const float lead = is_q ? rn * a.scale : rn * beta[i];
     const float rfac = bi > 0 ? lead * ex2_approx((Gi - Ghi[16 * bi - 1]) + (Gl - Glo[16 * bi - 1])) : 0.0f;
+    uint32_t marks = 0u;  // +-0 twice while this row's scores are finite
     // 8 values of this row from column j on: to A, or to the scores
     auto put = [&](int j, float (&f)[8], bool mine) {
       if (n < kC && !is_q && i >= n) {
@@ -648,6 +658,10 @@ __global__ void __launch_bounds__(128, 6)
           uint32_t hi[4], mi[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z) split2(sh, pk2(f[2 * z], f[2 * z + 1]), hi[z], mi[z]);
+          if constexpr (PAIR) {
+#pragma unroll
+            for (int z = 0; z < 4; ++z) marks = fma_bf16x2(hi[z], 0u, marks);
+          }
           unsigned char* p = img + kImgP + panel_piece(i, j >> 3);
           *reinterpret_cast<uint4*>(p) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           *reinterpret_cast<uint4*>(p + kPanelTerm) = make_uint4(mi[0], mi[1], mi[2], mi[3]);
@@ -697,6 +711,17 @@ __global__ void __launch_bounds__(128, 6)
         }
       }
       put(j, f, true);
+    }
+    if constexpr (PAIR) {
+      // Scores that are not finite in bf16 (decays above 1 or NaN) would meet zeros in the other head's rows: zeros
+      // take their place, and the row's output becomes NaN by its factor.
+      if (is_q && (marks & 0x7fff7fffu)) {
+        for (int j8 = 0; 8 * j8 <= (i | 15); ++j8) {
+          unsigned char* p = img + kImgP + panel_piece(i, j8);
+          *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(p + kPanelTerm) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        cf->oq[i] = __uint_as_float(0x7fffffffu);
+      }
     }
     __syncthreads();
     {  // rows 16 w .. of warp w: two 8 x 8 blocks, a column per lane (twice), then the block between them
@@ -1599,7 +1624,7 @@ template <int KA, bool PAIR>
 cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkPlan& p, void* ws, cudaStream_t st) {
   unsigned char* img = static_cast<unsigned char*>(ws);
   const int prep_smem = PrepSmem<KA>::kTotal + 1024, smem = ChainSmem<KA, PAIR>::kTotal + 1024;
-  auto prep = delta_prep_kernel<KA>;
+  auto prep = delta_prep_kernel<KA, PAIR>;
   // The kernels' shared-memory limits, once per device.
   static std::atomic<uint64_t> ready{0};
   int dev = 0;

@@ -1,0 +1,66 @@
+"""Edges of the gated delta rule: values that are not finite in one head of a
+pair. Tolerances as in test_delta_gpu.py.
+"""
+import math
+
+import pytest
+import torch
+
+from delta_util import inputs, rule
+from selective_state_space_depthwise_b200 import api
+from test_delta_gpu import check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    torch.cuda.init()
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("bad", [0, 1])
+@pytest.mark.parametrize("what,value", [("g", NAN), ("g", INF), ("g", 100.0), ("beta", NAN), ("beta", INF), ("v", NAN)])
+@pytest.mark.parametrize("form", ["one walk", "segments", "packed", "packed cut", "shares"])
+def test_a_head_that_is_not_finite_leaves_its_pair_alone(form, what, value, bad):
+    """Two heads of 64 value channels on one key group are walked together. A decay, beta or value of one that is not
+    finite, or decays that leave the range of fp32 within a chunk, must not reach the other."""
+    G, H, dk, dv = 1, 2, 128, 64
+    lens = {"one walk": [200], "segments": [2500], "packed": [70, 200, 33], "packed cut": [90, 2500, 130],
+            "shares": [1100] * 3}[form]
+    if form == "shares":
+        H = 160
+    packed = form.startswith("packed")
+    i = 1 if packed else 0           # the sequence with the bad value
+    t = 2 * lens[i] // 3
+    lead = (1, sum(lens)) if packed else (len(lens), lens[0])
+    x = inputs(lead, G, H, dk, dv, seed=len(form), decay=0.3, l2norm=True)
+    clean = {n: y.clone() for n, y in x.items()}
+    row, at = (0, sum(lens[:i]) + t) if packed else (0, t)
+    if what == "v":
+        x["v"][row, at, bad, 5] = value
+    else:
+        x[what][row, at, bad] = value
+    if packed:
+        cu = torch.tensor([sum(lens[:n]) for n in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
+        out, st = api.delta_prefill(**{n: y[0] for n, y in x.items()}, qk_l2norm=True, cu_seqlens=cu)
+        out = out[None]
+        seqs = [(0, sum(lens[:n]), sum(lens[:n + 1])) for n in range(len(lens))]
+    else:
+        out, st = api.delta_prefill(**x, qk_l2norm=True)
+        seqs = [(n, 0, lens[n]) for n in range(len(lens))]
+    torch.cuda.synchronize()
+    for n, (b, a, e) in enumerate(seqs):
+        want, wst = rule(**{m: y[b:b + 1, a:e] for m, y in clean.items()}, l2norm=True)
+        keep = [h for h in range(H) if n != i or h != bad]
+        check(out[b:b + 1, a:e, keep], st[n:n + 1, keep], want[:, :, keep], wst[:, keep], f"sequence {n}")
+        if n == i and not math.isfinite(value):
+            check(out[b:b + 1, a:a + t, bad], torch.zeros(1), want[:, :t, bad], torch.zeros(1), "before the value")
+            after, s = out[b, a + t:e, bad], st[n, bad]
+            if what == "v":
+                after, s = after[:, 5], s[5]
+            assert not torch.isfinite(after).any() and not torch.isfinite(s).any()
