@@ -233,9 +233,11 @@ ssm_status delta_args(const ssm_delta_dims* d, bool prefill, const void* q, cons
   auto tok = [](int64_t given, int64_t dense) { return given ? given : dense; };
   a->q_tok = tok(d->q_tok_stride, nk), a->k_tok = tok(d->k_tok_stride, nk), a->v_tok = tok(d->v_tok_stride, nv);
   a->o_tok = tok(d->out_tok_stride, nv), a->gb_tok = tok(d->gb_tok_stride, d->nheads);
-  a->q_seq = tok(d->q_seq_stride, L * a->q_tok), a->k_seq = tok(d->k_seq_stride, L * a->k_tok);
-  a->v_seq = tok(d->v_seq_stride, L * a->v_tok), a->o_seq = tok(d->out_seq_stride, L * a->o_tok);
-  a->gb_seq = tok(d->gb_seq_stride, L * a->gb_tok);
+  // Rows of a decode step are dense by default whatever the token strides, which it does not use.
+  auto seq = [&](int64_t given, int64_t token, int64_t row) { return given ? given : prefill ? L * token : row; };
+  a->q_seq = seq(d->q_seq_stride, a->q_tok, nk), a->k_seq = seq(d->k_seq_stride, a->k_tok, nk);
+  a->v_seq = seq(d->v_seq_stride, a->v_tok, nv), a->o_seq = seq(d->out_seq_stride, a->o_tok, nv);
+  a->gb_seq = seq(d->gb_seq_stride, a->gb_tok, d->nheads);
   const int64_t toks[4] = {a->q_tok, a->k_tok, a->v_tok, a->o_tok}, least[4] = {nk, nk, nv, nv};
   const int64_t seqs[4] = {a->q_seq, a->k_seq, a->v_seq, a->o_seq};
   for (int i = 0; i < 4; ++i) {

@@ -1,13 +1,14 @@
 """Edges of the gated delta rule: values that are not finite in one head of a
-pair. Tolerances as in test_delta_gpu.py.
+pair, decode rows at their default strides. Tolerances as in test_delta_gpu.py.
 """
+import ctypes
 import math
 
 import pytest
 import torch
 
 from delta_util import inputs, rule
-from selective_state_space_depthwise_b200 import api
+from selective_state_space_depthwise_b200 import _lib, api
 from test_delta_gpu import check
 
 pytestmark = pytest.mark.gpu
@@ -64,3 +65,27 @@ def test_a_head_that_is_not_finite_leaves_its_pair_alone(form, what, value, bad)
             if what == "v":
                 after, s = after[:, 5], s[5]
             assert not torch.isfinite(after).any() and not torch.isfinite(s).any()
+
+
+def test_decode_rows_do_not_follow_the_token_strides():
+    """The dims of a prefill out of a fused buffer, given to decode with dense rows: the rows are dense. (The buffers
+    are as long as rows at the token strides would be.)"""
+    lib = _lib.load()
+    b, G, H, dk, dv = 5, 2, 4, 64, 72
+    nk, nv, wide = G * dk, H * dv, 2 * G * dk + H * dv
+    x = inputs((b, 1), G, H, dk, dv, seed=5)
+    d = _lib.SsmDeltaDims(b, 9, H, G, dk, dv, 0.0, 0, wide, 0, wide, 0, wide, 0, wide, 0, H + 4, 0)
+
+    def rows(t, stride):
+        buf = torch.full((b * stride + 64,), 7.0, dtype=t.dtype, device="cuda")
+        buf[:t.numel()] = t.reshape(-1)
+        return buf
+
+    buf = {n: rows(t, H + 4 if n in ("g", "beta") else wide) for n, t in x.items()}
+    out = torch.full((b * wide + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(b, H, dv, dk, device="cuda")
+    _lib.check(lib.ssm_delta_decode_step(ctypes.byref(d), *(buf[n].data_ptr() for n in ("q", "k", "v", "g", "beta")),
+                                         None, b, st.data_ptr(), out.data_ptr(), st.data_ptr(), None))
+    torch.cuda.synchronize()
+    check(out[:b * nv].reshape(b, 1, H, dv), st, *rule(**x))
+    assert (out[b * nv:] == 7).all()
