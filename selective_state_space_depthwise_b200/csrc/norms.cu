@@ -140,12 +140,14 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 256) gated_norm_kernel(const Ga
   constexpr bool kKeepW = NV <= 2;
   const int team = BLOCK ? static_cast<int>(blockDim.x) : a.team;
   const int i0 = BLOCK ? threadIdx.x : threadIdx.x & (team - 1);
-  const uint32_t tid = BLOCK ? blockIdx.x : (blockIdx.x * blockDim.x + threadIdx.x) >> a.team_shift;
+  // the block's first team: counted in teams, since a row may have more threads than 32 bits count
+  const uint32_t team0 = BLOCK ? blockIdx.x : blockIdx.x * (blockDim.x >> a.team_shift);
+  const uint32_t tid = BLOCK ? team0 : team0 + (threadIdx.x >> a.team_shift);
   uint32_t grp, first_grp;
   uint32_t row = a.groups(tid, grp);
   const bool has = tid < a.active;
   // the block's threads make the same number of rounds: its first team's, whose rows come first
-  uint32_t round = BLOCK ? row : a.groups((blockIdx.x * blockDim.x) >> a.team_shift, first_grp);
+  uint32_t round = BLOCK ? row : a.groups(team0, first_grp);
   const float inv_n = 1.0f / static_cast<float>(a.group);
   const int64_t c0 = static_cast<int64_t>(grp) * a.group + i0 * VEC;
   const T* x = static_cast<const T*>(a.x) + c0;
