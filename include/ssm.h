@@ -490,7 +490,8 @@ ssm_status ssm_delta_prefill(const ssm_delta_dims *dims, const void *q, const vo
  *   q, k [b, ngroups, d_key] bf16, v [b, nheads, d_value] bf16, g, beta
  *   [b, nheads] fp32, out [b, nheads, d_value] bf16: row s at its seq stride,
  *   0 = dense rows (ngroups * d_key, nheads * d_value or nheads elements). The
- *   token strides are not used; they are checked as for a prefill.
+ *   token strides are not used; they are checked as for a prefill. Values that
+ *   are not finite act as in a prefill.
  *   state_index NULL (row s uses state s), or [b] int32 on the device: row s
  *               uses state state_index[s] of a pool of num_states. A row whose
  *               index is negative or >= num_states is padding: neither its

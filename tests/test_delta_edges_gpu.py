@@ -1,5 +1,6 @@
 """Edges of the gated delta rule: values that are not finite in one head of a
-pair, decode rows at their default strides. Tolerances as in test_delta_gpu.py.
+pair, decode rows at their default strides, keys whose squares overflow.
+Tolerances as in test_delta_gpu.py.
 """
 import ctypes
 import math
@@ -89,3 +90,23 @@ def test_decode_rows_do_not_follow_the_token_strides():
     torch.cuda.synchronize()
     check(out[:b * nv].reshape(b, 1, H, dv), st, *rule(**x))
     assert (out[b * nv:] == 7).all()
+
+
+@pytest.mark.parametrize("L", [1, 2, 17, 40, 64, 100, 2500])
+@pytest.mark.parametrize("l2norm", [False, True])
+@pytest.mark.parametrize("dk", [64, 128])
+def test_keys_whose_squares_overflow(L, l2norm, dk):
+    """A finite key with a sum of squares beyond fp32: as a key that is not finite, at every length."""
+    t, H, dv = 2 * L // 3, 2, 128
+    x = inputs((2, L), 1, H, dk, dv, seed=L, decay=0.1, l2norm=l2norm)
+    want, wst = rule(**x, l2norm=l2norm)
+    x["k"][0, t] = 1e20
+    out, st = api.delta_prefill(**x, qk_l2norm=l2norm)
+    check(out[:1, :t], torch.zeros(1), want[:1, :t], torch.zeros(1))
+    check(out[1:], st[1:], want[1:], wst[1:])
+    assert not torch.isfinite(out[0, t:]).any() and not torch.isfinite(st[0]).any()
+    if L == 1:
+        s0 = torch.zeros(2, H, dv, dk, device="cuda")
+        out = api.delta_decode_step(**{n: y[:, 0] for n, y in x.items()}, state=s0, qk_l2norm=l2norm)
+        check(out[1:, None], s0[1:], want[1:], wst[1:])
+        assert not torch.isfinite(out[0]).any() and not torch.isfinite(s0[0]).any()
