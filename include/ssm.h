@@ -476,8 +476,9 @@ typedef struct {
  *
  * Values that are not finite. From a token whose k (or its sum of squares in
  * fp32), g or beta is not finite on, its head's outputs and state are not
- * finite; of v, its row's; of q, only the token's output. Outputs before that
- * token, other sequences and heads are unaffected.
+ * finite; of v, its row's; of q (or, with qk_l2norm, its sum of squares), only
+ * the token's output. Outputs before that token, other sequences and heads are
+ * unaffected.
  */
 /* Workspace of a call with these dims, with (packed = 1) or without cu_seqlens; 0 for invalid dims. */
 size_t ssm_delta_prefill_workspace_bytes(const ssm_delta_dims *dims, int32_t packed);

@@ -130,12 +130,13 @@ __global__ void __launch_bounds__(32 * kRecWarps, BLOCKS) delta_recurrent_kernel
     }
     // The norms scale the products, not k and q: their sums are on the way while the products' are.
     // A key whose squares overflow makes rk NaN, and with it the update, as in the chunk kernels; without norms its
-    // sum is looked at where a lane's part is large.
+    // sum is looked at where a lane's part is large. Of a query with norms, rq.
     float rq = a.scale, rk = 1.0f;
     if (a.l2norm) {
       const float kk = group_sum<LPR>(dot4(k, k));
       rk = fmaf(kk, 0.0f, rsqrtf(kk + kL2Eps));
-      rq *= rsqrtf(group_sum<LPR>(dot4(q, q)) + kL2Eps);
+      const float qq = group_sum<LPR>(dot4(q, q));
+      rq *= fmaf(qq, 0.0f, rsqrtf(qq + kL2Eps));
     } else if (__any_sync(0xffffffffu, !(dot4(k, k) <= 1e37f))) {
       rk = fmaf(group_sum<LPR>(dot4(k, k)), 0.0f, 1.0f);
     }

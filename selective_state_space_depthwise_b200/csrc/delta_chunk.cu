@@ -601,6 +601,7 @@ __global__ void __launch_bounds__(128, 6)
     }
     k_bad = !(s0 + s1 <= 3.4028235e38f);
     if (a.l2norm) rn = rsqrtf(s0 + s1 + kL2Eps);
+    if (is_q) rn = fmaf(s0 + s1, 0.0f, rn);  // NaN where the squares overflow
   }
   if (!is_q) rk[i] = rn;
   wait(done, 0, 32);

@@ -1,6 +1,6 @@
 """Edges of the gated delta rule: values that are not finite in one head of a
-pair, decode rows at their default strides, keys whose squares overflow.
-Tolerances as in test_delta_gpu.py.
+pair, decode rows at their default strides, keys and queries whose squares
+overflow. Tolerances as in test_delta_gpu.py.
 """
 import ctypes
 import math
@@ -110,3 +110,22 @@ def test_keys_whose_squares_overflow(L, l2norm, dk):
         out = api.delta_decode_step(**{n: y[:, 0] for n, y in x.items()}, state=s0, qk_l2norm=l2norm)
         check(out[1:, None], s0[1:], want[1:], wst[1:])
         assert not torch.isfinite(out[0]).any() and not torch.isfinite(s0[0]).any()
+
+
+@pytest.mark.parametrize("L", [1, 17, 40, 64, 100, 2500])
+@pytest.mark.parametrize("dv", [64, 128])
+def test_queries_whose_squares_overflow(L, dv):
+    """A finite query with a sum of squares beyond fp32 has no norm: its output is not a number, and nothing else."""
+    t, H, dk = 2 * L // 3, 2, 128
+    x = inputs((2, L), 1, H, dk, dv, seed=L, l2norm=True)
+    want, wst = rule(**x, l2norm=True)
+    x["q"][0, t] = 1e20
+    out, st = api.delta_prefill(**x, qk_l2norm=True)
+    assert out[0, t].isnan().all()
+    out[0, t], want[0, t] = 0, 0
+    check(out, st, want, wst)
+    if L == 1:
+        s0 = torch.zeros(2, H, dv, dk, device="cuda")
+        out = api.delta_decode_step(**{n: y[:, 0] for n, y in x.items()}, state=s0, qk_l2norm=True)
+        assert out[0].isnan().all()
+        check(out[1:, None], s0, want[1:], wst)
