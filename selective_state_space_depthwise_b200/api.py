@@ -512,8 +512,8 @@ def _delta_dims(q, k, v, g, beta, out, scale, qk_l2norm, batch, seqlen, tokens, 
         raise ValueError("g and beta must be float32 with one value per token and head of v")
     if scale is None:
         scale = 0.0
-    elif not scale > 0:
-        raise ValueError("scale must be positive")
+    elif not 1e-45 < scale <= 3.4028234663852886e38:  # 0 in the dims is the default
+        raise ValueError("scale must be positive and finite in float32")
     if q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous() and g.is_contiguous() \
             and beta.is_contiguous():
         strides = ()
