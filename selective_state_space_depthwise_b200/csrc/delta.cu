@@ -66,7 +66,7 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, a.x * b.x)));
 }
 
-// One block: kRecWarps * kRecSteps * 32 / LPR rows of one (sequence, head).
+// One block: kRecWarps * kRecSteps * 32 / LPR rows of one (sequence, head). Never with packed tokens (takes_chunks).
 // One token: seven blocks an SM: the registers that this leaves spill a little, but a
 // decode step of 256 x 60 heads of 128 x 128 (2.03 GB) takes 301 us (6.75
 // TB/s) against 311 with six, 338 with five and 306 with eight.
@@ -86,27 +86,18 @@ __global__ void __launch_bounds__(32 * kRecWarps, BLOCKS) delta_recurrent_kernel
     slot = a.index[s];
     if (slot < 0 || slot >= a.num_states) return;  // padding
   }
-  // rows of this sequence: first row and count
-  int64_t t0 = 0, n = a.L, seq = s;
-  if (a.cu) {
-    const int64_t c0 = a.cu[s], c1 = a.cu[s + 1];
-    t0 = c0 < 0 ? 0 : c0 > a.L ? a.L : c0;
-    const int64_t t1 = c1 < t0 ? t0 : c1 > a.L ? a.L : c1;
-    n = t1 - t0, seq = 0;
-  }
-
   const int part = lane / LPR, c = (lane % LPR) * 4;
   const bool in = c < a.dk;
-  const __nv_bfloat16* qp = a.q + seq * a.q_seq + t0 * a.q_tok + grp * a.dk + c;
-  const __nv_bfloat16* kp = a.k + seq * a.k_seq + t0 * a.k_tok + grp * a.dk + c;
-  const float* gp = a.g + seq * a.gb_seq + t0 * a.gb_tok + h;
-  const float* bp = a.beta + seq * a.gb_seq + t0 * a.gb_tok + h;
+  const __nv_bfloat16* qp = a.q + s * a.q_seq + grp * a.dk + c;
+  const __nv_bfloat16* kp = a.k + s * a.k_seq + grp * a.dk + c;
+  const float* gp = a.g + s * a.gb_seq + h;
+  const float* bp = a.beta + s * a.gb_seq + h;
   // The reduction leaves product `mine` here: p of step mine (< kRecSteps) or w of step mine - kRecSteps.
   const int mine = lane % LPR / kLanes, step = mine % kRecSteps;
   const int my_row = row0 + step * kPar + part;
   const bool row_in = my_row < a.dv;
-  const __nv_bfloat16* vp = a.v + seq * a.v_seq + t0 * a.v_tok + h * a.dv + (row_in ? my_row : 0);
-  __nv_bfloat16* op = a.out + seq * a.o_seq + t0 * a.o_tok + h * a.dv + my_row;
+  const __nv_bfloat16* vp = a.v + s * a.v_seq + h * a.dv + (row_in ? my_row : 0);
+  __nv_bfloat16* op = a.out + s * a.o_seq + h * a.dv + my_row;
   const bool stores = row_in && mine >= kRecSteps && lane % kLanes == 0;
 
   float4 S[kRecSteps];
@@ -120,8 +111,9 @@ __global__ void __launch_bounds__(32 * kRecWarps, BLOCKS) delta_recurrent_kernel
   }
   float4 q{}, k{};
   float g = 0.f, b = 0.f, v = 0.f;
+  const int n = static_cast<int>(a.L);
   if (n > 0) q = load_bf16x4(qp, in), k = load_bf16x4(kp, in), g = *gp, b = *bp, v = __bfloat162float(*vp);
-  for (int64_t t = 0; t < n; ++t) {
+  for (int t = 0; t < n; ++t) {
     float4 qn{}, kn{};
     float gn = 0.f, bn = 0.f, vn = 0.f;
     if (t + 1 < n) {

@@ -129,3 +129,13 @@ def test_queries_whose_squares_overflow(L, dv):
         out = api.delta_decode_step(**{n: y[:, 0] for n, y in x.items()}, state=s0, qk_l2norm=True)
         assert out[0].isnan().all()
         check(out[1:, None], s0, want[1:], wst)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_packed_buffers_without_tokens_pass_the_states_on(given):
+    x = {n: t[0] for n, t in inputs((1, 0), 1, 2, 64, 128, seed=1).items()}
+    s0 = torch.randn(3, 2, 128, 64, device="cuda") if given else None
+    cu = torch.zeros(4, dtype=torch.int32, device="cuda")
+    out, st = api.delta_prefill(**x, cu_seqlens=cu, state_in=s0)
+    torch.cuda.synchronize()
+    assert out.shape == (0, 2, 128) and torch.equal(st, s0 if given else torch.zeros_like(st))
