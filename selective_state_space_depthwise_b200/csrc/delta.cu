@@ -210,11 +210,11 @@ ssm_status delta_shape(const ssm_delta_dims* d, bool prefill) {
 bool takes_chunks(const ssm_delta_dims& d, bool packed) {
   if (d.seqlen <= 0) return false;
   if (packed || d.seqlen >= kDeltaChunk) return true;
-  constexpr int64_t kSms = 148;
+  const int64_t sms = device_sms();
   const int64_t blocks = d.batch * d.nheads * recurrent_blocks(d.d_key, d.d_value);
-  const int64_t rounds = (d.batch * delta_walkers(d.nheads, d.ngroups, d.d_value) + kSms - 1) / kSms;
+  const int64_t rounds = (d.batch * delta_walkers(d.nheads, d.ngroups, d.d_value) + sms - 1) / sms;
   const bool pair = delta_pairs(d.nheads, d.ngroups, d.d_value);
-  const double token = 0.47 + (blocks > kSms ? 0.00145 * static_cast<double>(blocks - kSms) : 0.0);
+  const double token = 0.47 + (blocks > sms ? 0.00145 * static_cast<double>(blocks - sms) : 0.0);
   const double chunk = (pair ? 22.0 : 19.5) - (d.d_key <= 64 ? 3.0 : 0.0) +
                        (pair ? 16.5 : 13.0) * static_cast<double>(rounds - 1);
   return 2.3 + static_cast<double>(d.seqlen) * token > chunk;

@@ -1570,14 +1570,8 @@ struct ChunkPlan {
   size_t next, flags, cuts, S, M, bytes;  // offsets of what is not operand tiles, and the end
 };
 ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed) {
-  int dev = 0;
   ChunkPlan p{};
-  p.sms = 148;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || p.sms <= 0) {
-    cudaGetLastError();  // no device: the default SM count
-    p.sms = 148;
-  }
+  p.sms = device_sms();
   p.slots = chunk_slots(batch, L, packed);
   p.slices = static_cast<int>((dv + 127) / 128);
   p.pair = delta_pairs(H, G, dv);
@@ -1681,6 +1675,16 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
 }
 
 }  // namespace
+
+int device_sms() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      sms <= 0) {
+    cudaGetLastError();  // no device: a B200's
+    sms = 148;
+  }
+  return sms;
+}
 
 size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed) {
   return chunk_plan(batch, L, H, G, dk, dv, packed).bytes;

@@ -33,6 +33,9 @@ inline int64_t delta_walkers(int64_t H, int64_t G, int64_t dv) {
   return delta_pairs(H, G, dv) ? H / 2 : H * ((dv + 127) / 128);
 }
 
+// SMs of the current device.
+int device_sms();
+
 // 64 tokens at a time on the tensor cores; a.L > 0.
 cudaError_t launch_delta_chunk(const DeltaArgs& a, void* ws, cudaStream_t st);
 size_t delta_chunk_workspace(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk, int64_t dv, bool packed);
