@@ -469,7 +469,10 @@ typedef struct {
  *               256-byte aligned, or NULL when that is 0 (26 KB for each 64
  *               tokens and head, plus as much for each packed sequence; calls
  *               that may walk long sequences in segments keep a state and a
- *               d_key x d_key matrix for each segment and head besides).
+ *               d_key x d_key matrix for each segment and head besides, packed
+ *               ones for as many as their tokens may have: 32 a sequence and
+ *               1 + tokens / 512 at most, of sequences of more than 512 tokens).
+ *               For less, process long sequences in pieces, as below.
  *               Calls that overlap on the GPU need separate workspaces.
  * A long sequence may be processed in pieces: feeding one call's state_out to
  * the next gives the result of one call up to fp32 rounding.

@@ -46,6 +46,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "delta_internal.h"
@@ -251,6 +252,7 @@ struct Segments {
   int job, share;   // shares: chunks of a walk, and a block's part of the line of all walks; job 0: whole walks
   int walkers;      // walks of one segment of a sequence: its heads times the slices of d_value, or pairs of heads
   int sms;
+  int room;         // packed: segments that S and M hold
 };
 
 // Shares. Walks of one length, more than the SMs, are not handed out whole (320
@@ -300,15 +302,21 @@ struct Cut {
 
 // Time of a packed batch in chunks, cut into segments of `per`: the longest walk or the work of all over the SMs,
 // whichever is more, for both passes; launches as in choose_segments, and for each segment of the longest the join
-// (`join`: its blocks for one sequence, over the SMs).
+// (`join`: its blocks for one sequence, over the SMs). 3e38 where the cut sequences have more segments than there is
+// room for: offsets that do not ascend name rows twice.
 __device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int longest, int heads, int walkers, int sms,
-                                         float join) {
+                                         int room, float join) {
   float w1 = 0.0f, w2 = 0.0f;
+  int used = 0;
   for (int s = 0; s < n; ++s) {
     const int segs = (c.chunks[s] + per - 1) / per;
     w2 += static_cast<float>(c.chunks[s] * walkers);
-    if (segs > 1) w1 += static_cast<float>(((segs - 1) * walkers + (segs - 2) * heads) * per);
+    if (segs > 1) {
+      w1 += static_cast<float>(((segs - 1) * walkers + (segs - 2) * heads) * per);
+      used += segs;
+    }
   }
+  if (used > room) return 3.0e38f;
   const float scale = 1.0f / static_cast<float>(sms), len = static_cast<float>(per);
   const float second = fmaxf(len, w2 * scale + 0.3f * len) + 2.5f;
   if (per >= longest) return second;
@@ -317,7 +325,7 @@ __device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int long
 }
 
 // All threads of a block, with `c` in shared memory; ends with a barrier.
-__device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int sms, Cut& c) {
+__device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int sms, int room, Cut& c) {
   const int n = static_cast<int>(a.batch), tid = threadIdx.x;
   for (int s = tid; s < n; s += blockDim.x) c.all[s] = (span_of(a, s).len + kC - 1) / kC;
   __syncthreads();
@@ -331,12 +339,8 @@ __device__ __forceinline__ void delta_cut(const DeltaArgs& a, int walkers, int s
     const int longest = max(1, c.chunks[0]);
     const int per = (longest + tid) / (tid + 1);
     const float join = static_cast<float>(static_cast<int>(a.H) * ((static_cast<int>(a.dv) + 15) / 16)) / static_cast<float>(sms);
-    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms, join);
-    // Offsets that do not ascend name rows twice, and could ask for more segments than the workspace holds: no cut.
-    int64_t total = 0;
-    for (int i = 0; i < n; ++i) total += c.chunks[i];
-    const bool fits = total <= a.L / kC + n;
-    if (tid > 0) cost = per < kCutLeast || !fits ? 3.0e38f : cost * 1.05f;
+    float cost = cut_cost(c, n, per, longest, static_cast<int>(a.H), walkers, sms, room, join);
+    if (tid > 0) cost = per < kCutLeast ? 3.0e38f : cost * 1.05f;
     int best = tid;
     for (int m = 16; m > 0; m >>= 1) {
       const float oc = __shfl_xor_sync(0xffffffffu, cost, m);
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(128, 6)
   }
   int block = static_cast<int>(blockIdx.x);
   if (sg.cut && block-- == 0) {
-    delta_cut(a, sg.walkers, sg.sms, *reinterpret_cast<Cut*>(smem));
+    delta_cut(a, sg.walkers, sg.sms, sg.room, *reinterpret_cast<Cut*>(smem));
     copy_cut(reinterpret_cast<const Cut*>(smem), sg.cut);
     return;
   }
@@ -1565,7 +1569,7 @@ int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int64_t dv, in
 
 struct ChunkPlan {
   int64_t slots;
-  int slices, walkers, count, per, sms;
+  int slices, walkers, count, per, sms, room;
   bool cut, pair;
   size_t next, flags, cuts, S, M, bytes;  // offsets of what is not operand tiles, and the end
 };
@@ -1590,8 +1594,11 @@ ChunkPlan chunk_plan(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t dk,
   p.cuts = p.flags + (!packed && most > p.sms ? up(static_cast<size_t>(p.sms) * 4) : 0);
   p.S = p.M = p.bytes = p.cuts + (p.cut ? up(sizeof(Cut)) : 0);
   if (p.count > 1 || p.cut) {
-    // With a cut, only a sequence's last segment may be shorter than kCutLeast, and it has 32 segments at most.
-    const int64_t segs = !p.cut ? batch * p.count : batch + (p.slots / kCutLeast < 31 * batch ? p.slots / kCutLeast : 31 * batch);
+    // Of packed sequences only those that are cut have states here, and as the longest they come first. Each has more
+    // than kCutLeast chunks, only its last segment may be shorter than that, and it has 32 segments at most.
+    const int64_t m = std::min(batch, L / (kC * kCutLeast + 1));
+    const int64_t segs = !p.cut ? batch * p.count : std::min(32 * m, m + (L / kC + m) / kCutLeast);
+    p.room = static_cast<int>(segs);
     p.M = up(p.S + static_cast<size_t>(segs * H * dv * dk) * 4);
     p.bytes = up(p.M + static_cast<size_t>(segs * H * dk * dk) * 4);
   }
@@ -1644,7 +1651,7 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   const int64_t bh = a.batch * a.H, units = a.batch * p.walkers;
   Segments sg{p.count, p.per, p.cut ? reinterpret_cast<Cut*>(img + p.cuts) : nullptr, static_cast<int>(units * p.count), reinterpret_cast<float*>(img + p.S),
               reinterpret_cast<float*>(img + p.M), reinterpret_cast<uint32_t*>(img + p.next), reinterpret_cast<uint32_t*>(img + p.flags), 0, 0,
-              p.walkers, p.sms};
+              p.walkers, p.sms, p.room};
   auto share = [&](Segments& g, double scale) {  // never for packed sequences
     bool shares = false;
     if (!a.cu) walk_time(g.items, p.per, p.sms, scale, &shares);

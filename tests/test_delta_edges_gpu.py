@@ -139,3 +139,25 @@ def test_packed_buffers_without_tokens_pass_the_states_on(given):
     out, st = api.delta_prefill(**x, cu_seqlens=cu, state_in=s0)
     torch.cuda.synchronize()
     assert out.shape == (0, 2, 128) and torch.equal(st, s0 if given else torch.zeros_like(st))
+
+
+@pytest.mark.parametrize("lens", [
+    [513] * 60 + [8] * 100, [1100] * 9 + [1] * 200, [577, 5, 577, 64] * 20, [4000] + [513] * 30, [512] * 40 + [2100],
+])
+def test_packed_cuts_stay_inside_their_workspace(lens):
+    """Many packed sequences just long enough to be cut, next to shorter ones: results, and nothing behind the
+    workspace."""
+    T, n, G, H, dk, dv = sum(lens), len(lens), 1, 2, 64, 72
+    x = {m: t[0] for m, t in inputs((1, T), G, H, dk, dv, seed=T, decay=0.05).items()}
+    at = torch.tensor([0] + lens).cumsum(0)
+    need = api.delta_prefill_workspace_bytes(n, T, H, G, dk, dv, packed=True)
+    ws = torch.full((need + (1 << 20),), 0x5A, dtype=torch.uint8, device="cuda")
+    s0 = torch.randn(n, H, dv, dk, device="cuda")
+    out, st = api.delta_prefill(**x, cu_seqlens=at.int().cuda(), state_in=s0, workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0x5A).all()
+    for m in sorted(set(lens)):
+        which = [i for i in range(n) if lens[i] == m]
+        rows = torch.stack([torch.arange(at[i], at[i] + m) for i in which]).cuda()
+        want = rule(**{k: t[rows] for k, t in x.items()}, state=s0[which])
+        check(out[rows], st[which], *want, f"length {m}")

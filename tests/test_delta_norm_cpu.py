@@ -208,3 +208,15 @@ def test_a_workspace_must_be_contiguous():
         api._workspace(torch.empty(1, dtype=torch.uint8).expand(1024), 1024, torch.device("cpu"), None)
     w = torch.empty(64, dtype=torch.uint8)
     assert api._workspace(w, 64, w.device, None) is w and api._workspace(w, 65, w.device, None).numel() == 65
+
+
+def test_packed_workspace_holds_states_of_cut_sequences_only(lib):
+    """256 sequences of 128 tokens: at most 63 of more than 512 tokens lie in so many rows, with one segment each and
+    one more for 512 tokens; none of the others has a segment's state and matrix."""
+    b, H, dk, dv = 256, 32, 128, 128
+    L = b * 128
+    tiles = 26496 * H * (L // 64 + b)
+    cut = min(b, L // 513)
+    states = (cut + (L // 64 + cut) // 8) * H * (dv * dk + dk * dk) * 4
+    got = api.delta_prefill_workspace_bytes(b, L, H, H, dk, dv, packed=True)
+    assert tiles + states <= got <= tiles + states + (1 << 14)
