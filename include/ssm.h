@@ -519,8 +519,9 @@ ssm_status ssm_delta_decode_step(const ssm_delta_dims *dims, const void *q, cons
  * x, z, y [b, L, dim] io_dtype, element (s, t, e) at s*seq_stride +
  * t*tok_stride + e (strides 0 = dense, any value >= 0; token strides >= dim);
  * z may be NULL (no gate). w fp32: [dim], or [group] for every group alike
- * with shared_weight. y may be x or z (same strides). dim a multiple of group,
- * group <= 32768 (SSM_ERR_UNSUPPORTED above). fp32 sums; y rounded once.
+ * with shared_weight. y may be x or z (same strides; others are refused). dim
+ * a multiple of group, group <= 32768 (SSM_ERR_UNSUPPORTED above). fp32 sums; y
+ * rounded once.
  * Pointers need only their element's alignment; 16-byte aligned pointers with
  * strides and group multiples of 8 take vector loads.
  */
@@ -547,8 +548,8 @@ ssm_status ssm_gated_norm(const ssm_gated_norm_dims *dims, const void *x, const 
  * x, y [rows, dim] io_dtype; residual_in, residual_out [rows, dim]
  * residual_dtype; row strides in elements (0 = dim); w, post_w [dim] fp32.
  * y is the norm of r' before its rounding to residual_dtype. residual_out may
- * be residual_in (same stride) and may be NULL (not written); y may be x (same
- * stride), but not residual_out.
+ * be NULL (not written). Each result may lie over x or residual_in of its type
+ * and stride (others are refused), but y not over residual_out.
  * dim <= 32768 (SSM_ERR_UNSUPPORTED above). Alignment as for ssm_gated_norm.
  */
 typedef struct {

@@ -432,6 +432,12 @@ ssm_status ssm_gated_norm(const ssm_gated_norm_dims* d, const void* x, const voi
   if (!x || !w || !y) return fail(SSM_ERR_INVALID_ARG, "x, w or y is NULL");
   if (!aligned(x, e) || (z && !aligned(z, e)) || !aligned(y, e) || !aligned(w, 4))
     return fail(SSM_ERR_INVALID_ARG, "x, z, w or y is not aligned to its element");
+  // y may lie over x or z where each element is over its own; a stride of one token or sequence says nothing
+  auto apart = [&](const void* in, int64_t tok, int64_t seq) {
+    return in == y && ((d->seqlen > 1 && tok != a.y_tok) || (d->batch > 1 && seq != a.y_seq));
+  };
+  if (apart(x, a.x_tok, a.x_seq) || apart(z, a.z_tok, a.z_seq))
+    return fail(SSM_ERR_INVALID_ARG, "y over x or z must have its strides");
   a.x = x, a.z = z, a.w = w, a.y = y;
   a.seqlen = ssm::Divider(static_cast<uint32_t>(d->seqlen)), a.groups = ssm::Divider(static_cast<uint32_t>(groups));
   a.rows = static_cast<uint32_t>(d->batch * d->seqlen), a.group = static_cast<int>(d->group);
@@ -473,6 +479,13 @@ ssm_status ssm_residual_norm(const ssm_residual_norm_dims* d, const void* x, con
   const size_t e = ssm::dtype_bytes(d->io_dtype), er = ssm::dtype_bytes(d->residual_dtype);
   if (!x || !w || !y) return fail(SSM_ERR_INVALID_ARG, "x, w or y is NULL");
   if (y == residual_out) return fail(SSM_ERR_INVALID_ARG, "y and residual_out are the same buffer");
+  // a result may lie over an input where each element is over its own
+  auto apart = [&](const void* out, size_t eo, int64_t so, const void* in, size_t ei, int64_t si) {
+    return out && out == in && (eo != ei || (d->rows > 1 && so != si));
+  };
+  if (apart(y, e, a.y_st, x, e, a.x_st) || apart(y, e, a.y_st, residual_in, er, a.rin_st) ||
+      apart(residual_out, er, a.rout_st, x, e, a.x_st) || apart(residual_out, er, a.rout_st, residual_in, er, a.rin_st))
+    return fail(SSM_ERR_INVALID_ARG, "a result over an input must have its type and stride");
   if (!aligned(x, e) || !aligned(y, e) || !aligned(w, 4) || (post_w && !aligned(post_w, 4)) ||
       (residual_in && !aligned(residual_in, er)) || (residual_out && !aligned(residual_out, er)))
     return fail(SSM_ERR_INVALID_ARG, "a pointer is not aligned to its element");

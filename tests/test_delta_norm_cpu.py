@@ -220,3 +220,26 @@ def test_packed_workspace_holds_states_of_cut_sequences_only(lib):
     states = (cut + (L // 64 + cut) // 8) * H * (dv * dk + dk * dk) * 4
     got = api.delta_prefill_workspace_bytes(b, L, H, H, dk, dv, packed=True)
     assert tiles + states <= got <= tiles + states + (1 << 14)
+
+
+def test_norms_refuse_a_result_over_an_input_at_another_stride_or_type(lib):
+    """Rows of a result written over rows of an input that other blocks still read."""
+    def residual(x=FAKE, r=2 * FAKE, y=3 * FAKE, ro=4 * FAKE, **kw):
+        d = _lib.SsmResidualNormDims()
+        d.rows, d.dim, d.eps, d.residual_scale, d.io_dtype, d.residual_dtype = 4, 128, 1e-5, 1.0, 1, 1
+        for k, v in kw.items():
+            setattr(d, k, v)
+        return lib.ssm_residual_norm(ctypes.byref(d), x, r, FAKE, None, y, ro, None)
+
+    for kw in (dict(y=FAKE, y_stride=136), dict(y=FAKE, x_stride=136), dict(y=2 * FAKE, residual_dtype=0),
+               dict(y=2 * FAKE, residual_in_stride=256), dict(ro=FAKE, residual_dtype=0),
+               dict(ro=FAKE, residual_out_stride=144), dict(ro=2 * FAKE, residual_in_stride=256),
+               dict(y=2 * FAKE, residual_dtype=0, rows=1)):
+        assert residual(**kw) == _lib.SSM_ERR_INVALID_ARG, kw
+
+    def gated(x=FAKE, z=2 * FAKE, y=3 * FAKE, **kw):
+        return lib.ssm_gated_norm(ctypes.byref(gated_dims(**kw)), x, z, FAKE, y, None)
+
+    for kw in (dict(y=FAKE, y_tok_stride=136), dict(y=FAKE, x_seq_stride=512), dict(y=2 * FAKE, z_tok_stride=256),
+               dict(y=2 * FAKE, y_seq_stride=1024)):
+        assert gated(**kw) == _lib.SSM_ERR_INVALID_ARG, kw
