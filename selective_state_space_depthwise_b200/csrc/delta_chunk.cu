@@ -31,10 +31,18 @@
 // Precision. q, k and v are bf16 and enter exactly; the key norms, decays and
 // beta are fp32 factors of rows and columns, never folded into a bf16 operand.
 // S, R, U and T are fp32 and go to the tensor cores as three bf16 terms (their
-// sum is exact), as many products as pairs of terms above 2^-24. Only the output's own product takes
-// two terms (2^-16, against its rounding to bf16). The tensor core adds into
-// fp32 accumulators with truncation, so the state itself is added up in fp32
-// registers, and the accumulators hold one chunk's contribution at a time.
+// sum is exact), as many products as pairs of terms above 2^-24. Before that,
+// T's blocks beyond 8 x 8 are products of two tf32 terms an operand, which hold
+// all but one bit of it. The tensor core adds into fp32 accumulators with
+// truncation, so the state itself is added up in fp32 registers, and the
+// accumulators hold one chunk's contribution at a time. (State against float64
+// after 2048 tokens: 1.2e-7 of its norm; of one key throughout: 3.3e-6.)
+// Only the output's own product takes fewer: two terms of the scores and of U,
+// without the product of the two second ones, and two of S: 2^-17.3 of the
+// output's RMS before its rounding to bf16 (2^-9), so that one output in 230
+// rounds to the neighbour of what float64 rounds to (token by token one in
+// 9000). Third terms would need 5 KB more an image, for which the stages of a
+// pair leave no room, and columns of tensor memory, which is full.
 //
 // Values that are not finite: a product with a zero would spread them to tokens
 // before theirs. Those of a token's k, g and beta (found by the prep) and of v
@@ -413,9 +421,12 @@ struct PrepSmem {
   static constexpr int kTotal = kCf + 3 * kC * 4;
 };
 
-// A fp32 value as two tf32 ones: 11 bits, and the rest (13 bits, of which the product reads 11).
+// A fp32 value as two tf32 ones: 11 bits, rounded, and the rest (12 bits and a sign, of which the product reads 11).
+// Where keys are alike the entries of A are too, and what a product leaves out adds up over all tokens of a chunk: with
+// the first cut off, not rounded, and three products of terms, the state of 128 tokens of one key and beta = 1 was
+// 2.2e-5 off, so 4.1e-6, at 8 x 4096 tokens of 80 heads for 2.7% of the time (in fp32 FMAs 0.6e-6).
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -425,8 +436,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // One warp: the 16 x 8 NT block D = L R, L 16 x K and R K x 8 NT in As (row
-// stride kALd), K a multiple of 8; two tf32 terms each, three products (the
-// dropped one is 2^-22). 16-row blocks are far below the 128 rows of a
+// stride kALd), K a multiple of 8; two tf32 terms each, all four products.
+// 16-row blocks are far below the 128 rows of a
 // tcgen05 product, and in fp32 FMAs their operands' loads take the SM's whole
 // shared-memory bandwidth (4096 chunks and heads: 69 us with them, 59 us so; by
 // now 53).
@@ -447,6 +458,7 @@ __device__ __forceinline__ void block_product(const float* L, const float* R, in
       uint32_t bh[2], bl[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) split_tf32(R[(k + t + 4 * e) * kALd + 8 * j + g], bh[e], bl[e]);
+      mma_tf32(c[j], al, bl);
       mma_tf32(c[j], al, bh);
       mma_tf32(c[j], ah, bl);
       mma_tf32(c[j], ah, bh);
@@ -761,6 +773,7 @@ __global__ void __launch_bounds__(128, 6)
         split_tf32(R[t * kALd + g], bh[0], bl[0]);
         split_tf32(R[(t + 4) * kALd + g], bh[1], bl[1]);
         c[0] = c[1] = c[2] = c[3] = 0.0f;
+        mma_tf32(c, al, bl);
         mma_tf32(c, al, bh);
         mma_tf32(c, ah, bl);
         mma_tf32(c, ah, bh);

@@ -1,6 +1,7 @@
 """Edges of the gated delta rule: values that are not finite in one head of a
 pair, decode rows at their default strides, keys and queries whose squares
-overflow. Tolerances as in test_delta_gpu.py.
+overflow, packed cuts on their edges, correlated keys. Tolerances as in
+test_delta_gpu.py.
 """
 import ctypes
 import math
@@ -10,7 +11,7 @@ import torch
 
 from delta_util import inputs, rule
 from selective_state_space_depthwise_b200 import _lib, api
-from test_delta_gpu import check
+from test_delta_gpu import check, state0
 
 pytestmark = pytest.mark.gpu
 
@@ -161,3 +162,40 @@ def test_packed_cuts_stay_inside_their_workspace(lens):
         rows = torch.stack([torch.arange(at[i], at[i] + m) for i in which]).cuda()
         want = rule(**{k: t[rows] for k, t in x.items()}, state=s0[which])
         check(out[rows], st[which], *want, f"length {m}")
+
+
+@pytest.mark.parametrize("L", [64, 300, 2500])
+@pytest.mark.parametrize("noise", [0.0, 0.05, 0.5])
+@pytest.mark.parametrize("decay", [0.0, 0.1])
+def test_correlated_keys(L, noise, decay):
+    """Keys near plus or minus one direction and beta near 1: the chunk's system is then far from the identity, and its
+    inverse's terms cancel."""
+    b, G, H, dk, dv = 2, 1, 4, 128, 64
+    x = inputs((b, L), G, H, dk, dv, seed=L, decay=decay)
+    gen = torch.Generator().manual_seed(L)
+    sign = torch.randint(0, 2, (b, L, G, 1), generator=gen) * 2.0 - 1
+    k = sign * torch.randn(b, 1, G, dk, generator=gen) / dk ** 0.5
+    k = k + noise * torch.randn(b, L, G, dk, generator=gen) / dk ** 0.5
+    x["k"] = (k / k.square().sum(-1, keepdim=True).sqrt()).bfloat16().cuda()
+    x["beta"] = (1 - 0.02 * torch.rand(b, L, H, generator=gen)).cuda()
+    s0 = state0(b, H, dv, dk, 9)
+    out, st = api.delta_prefill(**x, state_in=s0)
+    check(out, st, *rule(**x, state=s0))
+
+
+@pytest.mark.parametrize("L", [64, 100, 128, 300, 2048])
+@pytest.mark.parametrize("noise", [0.0, 0.01, 0.05])
+@pytest.mark.parametrize("alternate", [False, True])
+def test_keys_alike_and_nothing_forgotten(L, noise, alternate):
+    """beta = 1, no decay and keys that are (nearly) one, with either sign: entries of the chunk's system are alike, and
+    what its products leave out would add up over the tokens instead of averaging out."""
+    b, G, H, dk, dv = 2, 8, 8, 128, 128
+    x = inputs((b, L), G, H, dk, dv, seed=L, decay=0.0)
+    gen = torch.Generator().manual_seed(7 * L)
+    k = torch.randn(b, 1, G, dk, generator=gen) / dk ** 0.5
+    if alternate:
+        k = k * (torch.randint(0, 2, (b, L, G, 1), generator=gen) * 2.0 - 1)
+    k = k + noise * torch.randn(b, L, G, dk, generator=gen) / dk ** 0.5
+    x["k"] = (k / k.square().sum(-1, keepdim=True).sqrt()).bfloat16().cuda()
+    x["beta"].fill_(1.0)
+    check(*api.delta_prefill(**x), *rule(**x))
