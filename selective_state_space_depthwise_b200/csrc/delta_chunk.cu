@@ -263,6 +263,11 @@ struct Segments {
   int room;         // packed: segments that S and M hold
 };
 
+// What the choices between whole walks, segments and shares count with, in chunks of a walk (3.4 us), as measured.
+constexpr double kWalkStart = 2.5;   // starting a walk
+constexpr double kStatesOnly = 0.85; // a chunk of pass 1, which forms no outputs
+constexpr double kMoreLaunches = 3.0;  // of pass 1 and the join
+
 // Shares. Walks of one length, more than the SMs, are not handed out whole (320
 // walks on 148 SMs would take three rounds, not 2.2) but laid end to end on a
 // line that is cut into equal shares, one a block. A walk across a cut begins in
@@ -273,7 +278,7 @@ struct Segments {
 // (8 sequences of 64 chunks, 80 heads in pairs: 723 us whole, 588 so; 32 heads of
 // 512 chunks in segments: both passes 937 and 827.) SHARE is a kernel of its own:
 // one that did both ways would walk whole ones 8% slower.
-constexpr int kStartChunks = 2;  // what starting a walk costs, in chunks
+constexpr int kStartChunks = 2;  // kWalkStart, in whole chunks: the line is counted in them
 constexpr int kShareLeast = 16;  // chunks of a walk that may be cut
 // The cut before share r: chunk `a` of walk `item`, on its first or last chunk where few would be left of one side.
 __device__ __forceinline__ void share_cut(const Segments& sg, int r, int& item, int& a) {
@@ -326,9 +331,10 @@ __device__ __forceinline__ float cut_cost(const Cut& c, int n, int per, int long
   }
   if (used > room) return 3.0e38f;
   const float scale = 1.0f / static_cast<float>(sms), len = static_cast<float>(per);
-  const float second = fmaxf(len, w2 * scale + 0.3f * len) + 2.5f;
+  constexpr float start = kWalkStart, more = kMoreLaunches, states = kStatesOnly;
+  const float second = fmaxf(len, w2 * scale + 0.3f * len) + start;
   if (per >= longest) return second;
-  return 0.85f * fmaxf(len, w1 * scale + 0.3f * len) + second + 5.5f +
+  return states * fmaxf(len, w1 * scale + 0.3f * len) + start + second + more +
          (0.4f + 0.7f * join) * static_cast<float>((longest + per - 1) / per - 2);
 }
 
@@ -1548,17 +1554,17 @@ int64_t chunk_slots(int64_t batch, int64_t L, bool packed) {
 // Rows of a join block: eight where such blocks fit the SMs at once.
 int join_rows(int64_t seq_heads, int64_t dv, int sms) { return seq_heads * ((dv + 7) / 8) <= sms ? 8 : 16; }
 
-// Time of `walks` walks of len chunks on `sms` SMs, in chunks (3.4 us): whole ones in rounds, each with 2.5 to start,
-// or equal shares of them (8% slower, and 3 for the hand-over), whichever is less. scale: of a chunk, 0.85 in pass 1.
+// Time of `walks` walks of len chunks on `sms` SMs, in chunks: whole ones in rounds, or equal shares of them (8%
+// slower, and 3 for the hand-over), whichever is less. scale: of a chunk, kStatesOnly in pass 1.
 double walk_time(int64_t walks, int64_t len, int sms, double scale, bool* shares) {
-  const double whole = static_cast<double>((walks + sms - 1) / sms) * (scale * static_cast<double>(len) + 2.5);
-  const double shared = static_cast<double>(walks) / sms * (1.08 * scale * static_cast<double>(len) + 2.5) + 3.0;
+  const double whole = static_cast<double>((walks + sms - 1) / sms) * (scale * static_cast<double>(len) + kWalkStart);
+  const double shared = static_cast<double>(walks) / sms * (1.08 * scale * static_cast<double>(len) + kWalkStart) + 3.0;
   *shares = walks > sms && len >= kShareLeast && shared < whole;
   return *shares ? shared : whole;
 }
 
 // Segments of a walk of nc chunks with `units` (sequence, head, slice) on
-// `sms` SMs: the time of both passes, 3 for the extra launches, and for each
+// `sms` SMs: the time of both passes and the extra launches, and for each
 // segment and wave of the join's blocks 0.4 (0.52 of 16 rows). (Times of 1 to
 // 32 segments for 2 to 60 heads and 2048 to 32768 tokens: the choice is within
 // 10% of the best.)
@@ -1573,8 +1579,8 @@ int choose_segments(int64_t nc, int64_t units, int64_t seq_heads, int64_t dv, in
   for (int64_t p = 2; p <= 64 && 4 * p <= nc && units * p <= 64 * sms; ++p) {
     const int64_t len = (nc + p - 1) / p;
     if ((nc + len - 1) / len != p) continue;
-    const double cost = walk_time(units * (p - 1) + seq_heads * (p - 2), len, sms, 0.85, &shares) +
-                        walk_time(units * p, len, sms, 1.0, &shares) + 3.0 + join * static_cast<double>(p - 2);
+    const double cost = walk_time(units * (p - 1) + seq_heads * (p - 2), len, sms, kStatesOnly, &shares) +
+                        walk_time(units * p, len, sms, 1.0, &shares) + kMoreLaunches + join * static_cast<double>(p - 2);
     if (cost < best) best = cost, count = static_cast<int>(p), *per = static_cast<int>(len);
   }
   return count;
@@ -1674,7 +1680,7 @@ cudaError_t launch_chunk(const ChunkMaps& maps, const DeltaArgs& a, const ChunkP
   };
   Segments first = sg;
   first.items = static_cast<int>(units * (p.count - 1) + bh * (p.count - 2));
-  if (p.count > 1) share(first, 0.85);
+  if (p.count > 1) share(first, kStatesOnly);
   share(sg, 1.0);
   Segments both = sg;
   both.job = sg.job | first.job;
