@@ -469,10 +469,10 @@ typedef struct {
  *               256-byte aligned, or NULL when that is 0 (26 KB for each 64
  *               tokens and head, plus as much for each packed sequence; calls
  *               that may walk long sequences in segments keep a state and a
- *               d_key x d_key matrix for each segment and head besides, packed
- *               ones for as many as their tokens may have: 32 a sequence and
- *               1 + tokens / 512 at most, of sequences of more than 512 tokens).
- *               For less, process long sequences in pieces, as below.
+ *               d_key x d_key matrix for each segment and head besides; only
+ *               packed sequences of more than 512 tokens are cut, into one
+ *               segment for 512 tokens and one more, and 32 at most). For less,
+ *               process long sequences in pieces, as below.
  *               Calls that overlap on the GPU need separate workspaces.
  * A long sequence may be processed in pieces: feeding one call's state_out to
  * the next gives the result of one call up to fp32 rounding.
@@ -500,8 +500,8 @@ ssm_status ssm_delta_prefill(const ssm_delta_dims *dims, const void *q, const vo
  *               uses state state_index[s] of a pool of num_states. A row whose
  *               index is negative or >= num_states is padding: neither its
  *               output nor any state is touched. Two rows of one call must not
- *               name the same state (which of them it then keeps is not
- *               specified).
+ *               name the same state: the parts of it, and in place the outputs
+ *               of either row, may then come from the one or the other.
  *   state_in    [num_states, nheads, d_value, d_key] fp32, dense
  *   state_out   the same shape; state_in itself for an update in place, or
  *               another pool (states of rows not named are left as they are).

@@ -67,9 +67,10 @@ __device__ __forceinline__ float dot4(float4 a, float4 b) {
 }
 
 // One block: kRecWarps * kRecSteps * 32 / LPR rows of one (sequence, head). Never with packed tokens (takes_chunks).
-// One token: seven blocks an SM: the registers that this leaves spill a little, but a
-// decode step of 256 x 60 heads of 128 x 128 (2.03 GB) takes 301 us (6.75
-// TB/s) against 311 with six, 338 with five and 306 with eight.
+// One token: seven blocks an SM. A decode step of 256 x 60 heads of 128 x 128
+// (2.03 GB) takes 301-325 us between boxes, 6.2-6.7 TB/s (on the best 301,
+// with six blocks 311, five 338, eight 306). Its 72 registers hold it all; with
+// up to 64 key channels 16 bytes spill.
 template <int LPR, int BLOCKS>
 __global__ void __launch_bounds__(32 * kRecWarps, BLOCKS) delta_recurrent_kernel(const DeltaArgs a, int row_blocks) {
   constexpr int kPar = 32 / LPR;           // rows of one step

@@ -407,9 +407,10 @@ __device__ __forceinline__ int cut_find(const int* sums, int n, int i) {
 // The inverse of I + A: 8 x 8 diagonal blocks by substitution (two a warp, a
 // column per lane), then the block below a pair of inverted ones, T21 = -T22
 // (A21 T11), for 8, 16 and 32 rows. (16 x 16 blocks by substitution, whose rows
-// every lane reads: 403 us for 8 sequences of 64 chunks and 80 heads, not 385.)
-// Shared memory's bandwidth (0.73 of it used) and instruction issue (0.64) bound
-// the kernel: 211 us for 8 sequences of 32 chunks and 80 heads, 500 MB.
+// every lane reads: 18 us more for 8 sequences of 64 chunks and 80 heads.)
+// Shared memory's bandwidth (0.67 of it used) and instruction issue (0.63) bound
+// the kernel: 217 us for 8 sequences of 32 chunks and 80 heads, 500 MB; 420 for
+// twice the chunks.
 constexpr int kPrepHeads = 4;
 constexpr int kALd = 68;  // floats between rows of A (16-byte rows, conflict-free columns)
 
@@ -445,8 +446,8 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 // stride kALd), K a multiple of 8; two tf32 terms each, all four products.
 // 16-row blocks are far below the 128 rows of a
 // tcgen05 product, and in fp32 FMAs their operands' loads take the SM's whole
-// shared-memory bandwidth (4096 chunks and heads: 69 us with them, 59 us so; by
-// now 53).
+// shared-memory bandwidth (4096 chunks and heads: 69 us with them when these
+// took 59).
 template <int K, int NT>
 __device__ __forceinline__ void block_product(const float* L, const float* R, int lane, float (&c)[NT][4]) {
   const int g = lane >> 2, t = lane & 3;

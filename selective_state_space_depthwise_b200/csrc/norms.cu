@@ -7,6 +7,14 @@
 // a time, so the second and third use of a value costs no traffic. The sums
 // are fp32, and each output is rounded once.
 //
+// The block-wide forms may have 1024 threads, so 64 registers each, and the
+// longest rows do not fit them: gated groups above 16384 channels spill 0.4-2
+// KB a thread (24576 channels, bf16: 3.1 TB/s, gate first 1.0; fp32 1.1), fp32
+// ones above 8192 200 bytes (4.6 TB/s), residual rows above 16384 60-220 bytes
+// (5.5-6.1 TB/s). Rows without vector loads are slower at every length (5001
+// channels, bf16: 1.5 and 4.1 TB/s; 20001: 0.5 and 1.6). The blocks of this
+// library have 2560 and 7680 channels.
+//
 // Teams. A gated group of up to 1024 channels is one team of 8, 16 or 32
 // lanes, and a block of 256 threads holds several; larger groups, and the rows
 // of the residual norm, are one block each (65536 x 2560 with a fp32 residual,
@@ -69,7 +77,8 @@ __device__ __forceinline__ float block_sum(float x, float* part) {
   return lanes_sum(lane < nw ? part[lane] : 0.0f, 32);
 }
 
-// n / d for 0 <= n < 2^31 without a division: d's rounded-up reciprocal, made once on the host.
+// n / d for 0 <= n < 2^31 without a division, by a multiplication with d's rounded-up reciprocal, made once on the
+// host (Granlund and Montgomery, Division by Invariant Integers using Multiplication, 1994).
 struct Divider {
   uint32_t d, mul, shift;
   explicit Divider(uint32_t div = 1) : d(div), mul(0), shift(0) {
